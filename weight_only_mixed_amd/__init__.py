@@ -12,6 +12,8 @@ from dataclasses import dataclass
 
 import torch
 
+from . import serve
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libslq.so")
 
@@ -95,6 +97,7 @@ def lib():
                   "slq_ear_kl", "slq_ear_kl_topk", "slq_mckp_search", "slq_gptq_quantize",
                   "slq_quant_error"):
             getattr(L, f).restype = _int
+        serve.declare(L)
         _LIB = L
     return _LIB
 
@@ -363,7 +366,11 @@ def slq_quant_error(W: torch.Tensor, pw: PackedWeight) -> torch.Tensor:
     return out
 
 
+from .serve import (KvCache, KvSeqs, alloc_kv_cache, slq_kv_attention, slq_kv_read,  # noqa: E402
+                    slq_kv_write, slq_sample, SLQ_BF16, SLQ_F16, SLQ_F32, SLQ_KV_E4M3, SLQ_KV_INT8)
+
 __all__ = ["lib", "SlqError", "SlqPacked", "PackedWeight", "alloc_packed", "workspace",
            "gemm_workspace_bytes", "kernel_name", "slq_quantize_pack", "slq_dequantize", "slq_dequant_gemm",
            "slq_row_lse", "slq_ear_kl", "slq_ear_kl_topk", "slq_mckp_search", "slq_gptq_quantize", "slq_quant_error",
+           *serve.__all__,
            "SLQ_META_F32", "SLQ_META_COMPACT", "SLQ_ASYM", "SLQ_SYM", "GROUP"]

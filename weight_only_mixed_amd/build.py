@@ -20,11 +20,13 @@ EXTRA = {"quantize.hip": ["-ffp-contract=off"],
          # GPTQ's column pass matches the oracle operation for operation: every
          # fused multiply-add is written out, nothing else may be contracted
          "gptq.hip": ["-ffp-contract=off"],
+         # cache codes are bit-exact IEEE, as the weight codes are
+         "kv_cache.hip": ["-ffp-contract=off"],
          # MFMA results in VGPRs: the decode epilogue reads them with plain VALU ops
          "gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 SOURCES = ["quantize.hip", "gemv.hip", "gemm.hip", "fidelity.hip", "mckp.hip", "gptq.hip", "probe.hip",
-           "noalloc.hip",
-           "slq_abi.cpp"]
+           "noalloc.hip", "kv_cache.hip", "kv_attention.hip", "sample.hip",
+           "slq_abi.cpp", "serve_abi.cpp"]
 
 
 def _compile(src: str) -> str:

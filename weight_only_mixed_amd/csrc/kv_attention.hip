@@ -1,0 +1,517 @@
+// Causal attention of ragged queries over the paged 8-bit cache.
+//
+//   s_j = scale * sk(page j) * (q . kcode_j),  p = softmax(s),
+//   o   = sum_j p_j * sv(page j) * vcode_j
+//
+// The query heads that share a kv head are rows of one product (row = query *
+// group + head in group), so each cached byte is read once per kv head.
+// Codes go to binary16 (exact: at most 8 significant bits, |code| <= 448) and
+// feed 16x16x32 MFMAs; q goes there too, after its row is shifted by a power
+// of two to a largest element in [1, 2), which keeps every product exact down
+// to 2^-25 of the row's largest element whatever the range of q.
+//
+// Scores are computed transposed, S^T = K q^T (rows: tokens, columns:
+// queries): lane l then holds, for query l % 16, tokens 4 (l/16) + v of each
+// 16-token tile, which is the operand layout of the second product
+// O^T = V^T P^T if its 32 k slots are numbered as the tokens of two such tiles
+// (slot 8 g + t: token 4 g + t of tile 0 for t < 4, token 4 g + t - 4 of tile
+// 1 above).  So probabilities never leave their lane, and the softmax
+// statistics of a query live in the lanes that hold its accumulators.  V rows
+// are loaded token by token, each lane taking the same dim / 16 bytes of the 8
+// tokens of its slots; the byte transposition is part of the conversion.
+// Nothing passes through shared memory before the epilogue.
+//
+// Probabilities enter the second product as binary16 of p * 2^15 * sv / R with
+// R the largest sv met so far (folded into the accumulator when it grows):
+// values down to 2^-39 of the largest still count.
+#include <float.h>
+
+#include <algorithm>
+#include <utility>
+
+#include "serve.h"
+#include "slq_device.h"
+
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+
+namespace slq {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kBlock = 32;            // tokens per wave and step
+constexpr float kPUnit = 32768.f;     // probabilities are held times this
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp2_hw(float v) { return __builtin_amdgcn_exp2f(v); }
+
+__device__ __forceinline__ f32x4_t mfma16h(u32x4_t a, u32x4_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a),
+                                                __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t h2_bits(f16x2_t v) { return __builtin_bit_cast(uint32_t, v); }
+
+// 1024 + (b + 128) in both halves, minus 1152: two signed bytes as binary16.
+// `v`: the bytes in bits 0..7 and 16..23, zero elsewhere.
+__device__ __forceinline__ uint32_t int8_pair(uint32_t v) {
+  const f16x2_t bias = {(_Float16)1152.f, (_Float16)1152.f};
+  return h2_bits(__builtin_bit_cast(f16x2_t, v ^ 0x64806480u) - bias);
+}
+
+// Four codes of a word as binary16.
+template <bool E4M3>
+__device__ __forceinline__ u32x2_t codes4(uint32_t w) {
+  u32x2_t r;
+  if constexpr (E4M3) {
+    r[0] = h2_bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, 1.0f, false));
+    r[1] = h2_bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, 1.0f, true));
+  } else {
+    r[0] = int8_pair(perm(0u, w, 0x0c010c00u));
+    r[1] = int8_pair(perm(0u, w, 0x0c030c02u));
+  }
+  return r;
+}
+
+// Column c (0..3) of two words of different tokens: (a's byte c, b's byte c).
+// E4M3 converts the pairs of columns 0/1 and 2/3 of one permuted word.
+template <bool E4M3, int C>
+__device__ __forceinline__ uint32_t column_pair(uint32_t a, uint32_t b) {
+  if constexpr (E4M3) {
+    const uint32_t w = C < 2 ? perm(b, a, 0x05010400u) : perm(b, a, 0x07030602u);
+    return h2_bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, 1.0f, (C & 1) != 0));
+  } else {
+    return int8_pair(perm(b, a, 0x0c000c00u | (uint32_t)C | (uint32_t)(4 + C) << 16));
+  }
+}
+
+template <typename F, int... I>
+__device__ __forceinline__ void for_each_int(F &f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+
+__device__ __forceinline__ float shfl_x(float v, int o) { return __shfl_xor(v, o, kWave); }
+// Over the four lanes that hold one query (l, l^16, l^32, l^48).
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, shfl_x(v, 16));
+  return fmaxf(v, shfl_x(v, 32));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += shfl_x(v, 16);
+  return v + shfl_x(v, 32);
+}
+
+__device__ __forceinline__ uint16_t to_out(float v, bool bf16) {
+  return bf16 ? __builtin_bit_cast(uint16_t, (__bf16)v) : __builtin_bit_cast(uint16_t, (_Float16)v);
+}
+
+// What the workgroups of one (sequence, tile of query rows) share: the token
+// range and how many splits of it hold any token.
+struct TileRange {
+  int lo, hi, start, active;
+};
+__device__ __forceinline__ TileRange tile_range(const KvAttnArgs &a, const KvSpan &sp, int rho0,
+                                                int rho1) {
+  const KvRange r = kv_visible(sp, a.window, rho0 / a.group, (rho1 - 1) / a.group);
+  TileRange t;
+  t.lo = r.lo;
+  t.hi = r.hi;
+  t.start = r.lo & ~(kBlock - 1);
+  t.active = r.hi > r.lo ? min((r.hi - t.start + a.chunk - 1) / a.chunk, a.splits) : 0;
+  return t;
+}
+
+template <int D, bool E4M3, int NT>
+__global__ __launch_bounds__(kThreads) void kv_attn_kernel(KvAttnArgs a) {
+  constexpr int KS = D / 32;      // MFMA k steps of q . k
+  constexpr int VJ = D / 16;      // bytes of a V row per lane, and MFMAs of p . v
+  constexpr int KL = D / 64;      // 16-byte K loads per token and lane
+  constexpr int VW = VJ / 4;      // 32-bit words of a V row per lane
+  constexpr int ROWS = 16 * NT;
+  constexpr int OP = D + 4;       // pitch of a query's outputs in LDS
+  __shared__ float o_lds[kWaves][16 * OP];
+  __shared__ float m_lds[kWaves][16], l_lds[kWaves][16];
+
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int col = lane & 15, g = lane >> 4;
+  const int b = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
+  const int h = blockIdx.y;
+  const KvSpan sp = kv_span(a.s, a.c.shift, b);
+  const int total = sp.n * a.group;
+  const uint8_t *kbase = a.c.codes[0] + (int64_t)h * a.c.head_stride;
+  const uint8_t *vbase = a.c.codes[1] + (int64_t)h * a.c.head_stride;
+
+  for (int rho0 = blockIdx.z * ROWS; rho0 < total; rho0 += a.tiles * ROWS) {
+    const int rho1 = min(rho0 + ROWS, total);
+    const TileRange tr = tile_range(a, sp, rho0, rho1);
+    if (split >= max(tr.active, a.splits == 1 ? 1 : 0)) continue;   // nothing here (uniform)
+    const int t0 = tr.start + split * a.chunk;
+    const int t1 = split == a.splits - 1 ? tr.hi : min(tr.hi, t0 + a.chunk);
+
+    // queries: lane (col, g) holds dims 64 h2 + 16 g + 8 e + t of query col
+    u32x4_t qf[NT][KS];
+    float qs[NT];
+    int pos[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int rho = rho0 + 16 * n + col;
+      const bool ok = rho < rho1;
+      const int i = (ok ? rho : rho0) / a.group, hd = (ok ? rho : rho0) % a.group;
+      pos[n] = ok ? sp.pos0 + i : -1;
+      const uint16_t *qp = a.q + (int64_t)(sp.row0 + i) * a.q_row +
+                           (int64_t)(h * a.group + hd) * a.q_head + 16 * g;
+      u32x4_t raw[KS];
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+        raw[k] = ok ? *reinterpret_cast<const u32x4_t *>(qp + 64 * (k >> 1) + 8 * (k & 1))
+                    : u32x4_t{0, 0, 0, 0};
+      qs[n] = a.scale_log2;
+      if (a.bf16) {
+        float mx = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            mx = fmaxf(mx, fmaxf(__builtin_bit_cast(float, (raw[k][w] << 16) & 0x7FFFFFFFu),
+                                 __builtin_bit_cast(float, raw[k][w] & 0x7FFF0000u)));
+        mx = quad_max(mx);
+        const int e = (int)(__builtin_bit_cast(uint32_t, mx) >> 23) - 127;
+        const float down = ldexpf(1.f, -(e / 2)), down2 = ldexpf(1.f, -(e - e / 2));
+        qs[n] = a.scale_log2 * ldexpf(1.f, e / 2) * ldexpf(1.f, e - e / 2);
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float lo = __builtin_bit_cast(float, raw[k][w] << 16) * down * down2;
+            const float hi = __builtin_bit_cast(float, raw[k][w] & 0xFFFF0000u) * down * down2;
+            qf[n][k][w] = h2_bits(f16x2_t{(_Float16)lo, (_Float16)hi});
+          }
+      } else {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) qf[n][k] = raw[k];
+      }
+    }
+
+    f32x4_t acc[NT][VJ];
+    float m[NT], l[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n] = -FLT_MAX;
+      l[n] = 0.f;
+#pragma unroll
+      for (int j = 0; j < VJ; ++j) acc[n][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    float unit = 0.f, inv_unit = 0.f;   // R and 2^15 / R
+    // tokens every query of this tile sees
+    const int all_hi = min(tr.hi, sp.pos0 + rho0 / a.group + 1);
+    const int last_pos = sp.pos0 + (rho1 - 1) / a.group;
+    const int all_lo = a.window > 0 ? max(tr.lo, last_pos - a.window + 1) : tr.lo;
+
+    for (int blk = t0 + kBlock * wave; blk < t1; blk += kBlock * kWaves) {
+      // the two 16-token tiles: their pages (a tile never crosses a page)
+      int id[2];
+      float sk[2], sv[2];
+      u32x4_t kw[2][KL];
+      uint32_t vw[2][4][VW];
+      bool plain = blk >= all_lo && blk + kBlock <= all_hi;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int tok = blk + 16 * u;
+        // a tile wholly outside the visible range is not looked at: its page may
+        // belong to someone else by now
+        id[u] = tok < tr.hi && tok + 16 > tr.lo ? kv_page(a.s, a.c.pages, b, tok >> a.c.shift) : -1;
+        plain = plain && id[u] >= 0;
+        const int64_t at = (int64_t)max(id[u], 0) * a.c.page_stride +
+                           (int64_t)(tok & ((1 << a.c.shift) - 1)) * a.c.token_stride;
+        sk[u] = sv[u] = 0.f;
+        if (id[u] >= 0) {
+          sk[u] = a.c.scales[0][(int64_t)id[u] * a.c.heads + h];
+          sv[u] = a.c.scales[1][(int64_t)id[u] * a.c.heads + h];
+          const uint8_t *kp = kbase + at + (int64_t)col * a.c.token_stride + 16 * g;
+          const uint8_t *vp = vbase + at + (int64_t)(4 * g) * a.c.token_stride + VJ * col;
+#pragma unroll
+          for (int k = 0; k < KL; ++k) kw[u][k] = *reinterpret_cast<const u32x4_t *>(kp + 64 * k);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint8_t *row = vp + (int64_t)t * a.c.token_stride;
+            if constexpr (VW == 1) vw[u][t][0] = *reinterpret_cast<const uint32_t *>(row);
+            else if constexpr (VW == 2) {
+              const u32x2_t w = *reinterpret_cast<const u32x2_t *>(row);
+              vw[u][t][0] = w[0];
+              vw[u][t][1] = w[1];
+            } else {
+              const u32x4_t w = *reinterpret_cast<const u32x4_t *>(row);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) vw[u][t][i] = w[i];
+            }
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < KL; ++k) kw[u][k] = u32x4_t{0, 0, 0, 0};
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < VW; ++i) vw[u][t][i] = 0u;
+        }
+      }
+      if (!plain) {   // rows outside every query's range may hold anything: 0 * NaN
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const int tok = blk + 16 * u + 4 * g + t;
+            const bool in = tok >= tr.lo && tok < tr.hi;
+#pragma unroll
+            for (int i = 0; i < VW; ++i) vw[u][t][i] = in ? vw[u][t][i] : 0u;
+          }
+      }
+      const float grown = fmaxf(unit, fmaxf(sv[0], sv[1]));
+      if (grown > unit) {
+        const float f = unit / grown;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < VJ; ++j) acc[n][j] *= f;
+        unit = grown;
+        inv_unit = kPUnit / grown;
+      }
+
+      f32x4_t s[NT][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[n][u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const u32x2_t c0 = codes4<E4M3>(kw[u][k >> 1][2 * (k & 1)]);
+          const u32x2_t c1 = codes4<E4M3>(kw[u][k >> 1][2 * (k & 1) + 1]);
+          const u32x4_t kf = {c0[0], c0[1], c1[0], c1[1]};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) s[n][u] = mfma16h(kf, qf[n][k], s[n][u]);
+        }
+      }
+      u32x4_t pf[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float f = sk[u] * qs[n];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) s[n][u][v] *= f;
+        }
+        if (!plain) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const int tok = blk + 16 * u + 4 * g + v;
+              const bool in = id[u] >= 0 && tok <= pos[n] && tok < tr.hi && tok >= tr.lo &&
+                              (a.window <= 0 || tok > pos[n] - a.window);
+              s[n][u][v] = in ? s[n][u][v] : -INFINITY;
+            }
+        }
+        float mx = s[n][0][0];
+#pragma unroll
+        for (int v = 1; v < 8; ++v) mx = fmaxf(mx, s[n][v >> 2][v & 3]);
+        if (__any(mx > m[n])) {
+          const float mn = fmaxf(m[n], quad_max(mx));
+          const float f = exp2_hw(m[n] - mn);
+          l[n] *= f;
+#pragma unroll
+          for (int j = 0; j < VJ; ++j) acc[n][j] *= f;
+          m[n] = mn;
+        }
+        float p[8];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          p[v] = exp2_hw(s[n][v >> 2][v & 3] - m[n]);
+          l[n] += p[v];
+          p[v] *= sv[v >> 2] * inv_unit;
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          pf[n][w] = h2_bits(f16x2_t{(_Float16)p[2 * w], (_Float16)p[2 * w + 1]});
+      }
+      auto column = [&](auto jc) {
+        constexpr int J = decltype(jc)::value, I = J / 4, C = J % 4;
+        const u32x4_t vf = {column_pair<E4M3, C>(vw[0][0][I], vw[0][1][I]),
+                            column_pair<E4M3, C>(vw[0][2][I], vw[0][3][I]),
+                            column_pair<E4M3, C>(vw[1][0][I], vw[1][1][I]),
+                            column_pair<E4M3, C>(vw[1][2][I], vw[1][3][I])};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[n][J] = mfma16h(vf, pf[n], acc[n][J]);
+      };
+      for_each_int(column, std::make_integer_sequence<int, VJ>());
+    }
+
+    // the four waves' parts of each query, joined in wave order
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float lt = quad_sum(l[n]), f = unit * (1.f / kPUnit);
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+#pragma unroll
+        for (int j = 0; j < VJ; j += 4)
+          *reinterpret_cast<f32x4_t *>(&o_lds[wave][col * OP + (4 * g + v) * VJ + j]) =
+              f32x4_t{acc[n][j][v] * f, acc[n][j + 1][v] * f, acc[n][j + 2][v] * f,
+                      acc[n][j + 3][v] * f};
+      if (g == 0) {
+        m_lds[wave][col] = m[n];
+        l_lds[wave][col] = lt;
+      }
+      __syncthreads();
+      const int qc = threadIdx.x / 16, d0 = (threadIdx.x % 16) * VJ;
+      const int rho = rho0 + 16 * n + qc;
+      if (rho < rho1) {
+        float mt = m_lds[0][qc];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) mt = fmaxf(mt, m_lds[w][qc]);
+        float lsum = 0.f, o[VJ] = {};
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          const float f2 = l_lds[w][qc] > 0.f ? exp2_hw(m_lds[w][qc] - mt) : l_lds[w][qc];
+          lsum += f2 * l_lds[w][qc];
+#pragma unroll
+          for (int j = 0; j < VJ; ++j) o[j] += f2 * o_lds[w][qc * OP + d0 + j];
+        }
+        const bool none = lsum == 0.f;
+        const float inv = none ? 0.f : 1.f / lsum;
+        const float lse2 = none ? -INFINITY : mt + log2f(lsum);
+        const int i = rho / a.group, hd = rho % a.group;
+        const int64_t row = (int64_t)(sp.row0 + i) * a.heads_q + h * a.group + hd;
+        if (a.splits == 1) {
+          uint16_t *op = a.out + row * D + d0;
+          union {
+            uint16_t e[VJ];
+            u32x2_t w[VJ / 4];
+          } t;
+#pragma unroll
+          for (int j = 0; j < VJ; ++j) t.e[j] = to_out(o[j] * inv, a.bf16);
+#pragma unroll
+          for (int j = 0; j < VJ / 4; ++j) reinterpret_cast<u32x2_t *>(op)[j] = t.w[j];
+          if (a.lse && d0 == 0) a.lse[row] = lse2 * kLn2;
+        } else {
+          const int64_t at = (int64_t)split * a.s.rows * a.heads_q + row;
+#pragma unroll
+          for (int j = 0; j < VJ; j += 4)
+            *reinterpret_cast<f32x4_t *>(a.part_o + at * D + d0 + j) =
+                f32x4_t{o[j] * inv, o[j + 1] * inv, o[j + 2] * inv, o[j + 3] * inv};
+          if (d0 == 0) a.part_lse[at] = lse2;
+        }
+      }
+    }
+  }
+}
+
+// Joins the splits of each query in split order.  A query whose tile had no
+// token (no split was active) gets 0 and -inf.
+template <int D, int NT>
+__global__ __launch_bounds__(kThreads) void kv_attn_join_kernel(KvAttnArgs a) {
+  constexpr int ROWS = 16 * NT, TPR = D / 4;   // threads per query row
+  const int b = blockIdx.x, h = blockIdx.y;
+  const KvSpan sp = kv_span(a.s, a.c.shift, b);
+  const int total = sp.n * a.group;
+  for (int rho0 = blockIdx.z * ROWS; rho0 < total; rho0 += a.tiles * ROWS) {
+    const int rho1 = min(rho0 + ROWS, total);
+    const TileRange tr = tile_range(a, sp, rho0, rho1);
+    for (int rho = rho0 + threadIdx.x / TPR; rho < rho1; rho += kThreads / TPR) {
+      const int d0 = (threadIdx.x % TPR) * 4;
+      const int i = rho / a.group, hd = rho % a.group;
+      const int64_t row = (int64_t)(sp.row0 + i) * a.heads_q + h * a.group + hd;
+      const int64_t step = (int64_t)a.s.rows * a.heads_q;
+      float m = -INFINITY;
+      for (int s = 0; s < tr.active; ++s) m = fmaxf(m, a.part_lse[s * step + row]);
+      float lsum = 0.f;
+      f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+      if (m != -INFINITY)
+        for (int s = 0; s < tr.active; ++s) {
+          const float e = a.part_lse[s * step + row];
+          const float f = e == -INFINITY ? 0.f : exp2_hw(e - m);
+          lsum += f;
+          o += *reinterpret_cast<const f32x4_t *>(a.part_o + (s * step + row) * D + d0) * f;
+        }
+      const float inv = lsum > 0.f ? 1.f / lsum : lsum == 0.f ? 0.f : lsum;
+      union {
+        uint16_t e[4];
+        u32x2_t w;
+      } t;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t.e[j] = to_out(o[j] * inv, a.bf16);
+      *reinterpret_cast<u32x2_t *>(a.out + row * D + d0) = t.w;
+      if (a.lse && d0 == 0) a.lse[row] = lsum == 0.f ? -INFINITY : (m + log2f(lsum)) * kLn2;
+    }
+  }
+}
+
+template <int D, int NT>
+hipError_t launch_nt(const KvAttnArgs &a, bool e4m3, hipStream_t st) {
+  const dim3 grid((unsigned)a.s.batch * (unsigned)a.splits, (unsigned)a.c.heads, (unsigned)a.tiles);
+  if (e4m3)
+    hipLaunchKernelGGL((kv_attn_kernel<D, true, NT>), grid, dim3(kThreads), 0, st, a);
+  else
+    hipLaunchKernelGGL((kv_attn_kernel<D, false, NT>), grid, dim3(kThreads), 0, st, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  hipLaunchKernelGGL((kv_attn_join_kernel<D, NT>),
+                     dim3((unsigned)a.s.batch, (unsigned)a.c.heads, (unsigned)a.tiles),
+                     dim3(kThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_dim(const KvAttnArgs &a, bool e4m3, int nt, hipStream_t st) {
+  switch (nt) {
+    case 1: return launch_nt<D, 1>(a, e4m3, st);
+    case 2: return launch_nt<D, 2>(a, e4m3, st);
+    default:
+      if constexpr (D == 256) return launch_nt<D, 2>(a, e4m3, st);
+      else return launch_nt<D, 4>(a, e4m3, st);
+  }
+}
+
+}  // namespace
+
+KvAttnPlan kv_attn_plan(int batch, int heads, int dim, int64_t capacity, int64_t rows, int heads_q,
+                        int window, int64_t max_q, int64_t max_len) {
+  KvAttnPlan p{};
+  const int64_t group = heads_q / heads;
+  const int64_t q = std::min(max_q, rows);
+  const int64_t qrows = q * group;
+  p.nt = qrows <= 16 ? 1 : qrows <= 32 || dim == 256 ? 2 : 4;
+  p.tiles = (int)std::min<int64_t>((qrows + 16 * p.nt - 1) / (16 * p.nt), 65535);
+  int64_t span = std::min(max_len, capacity);
+  if (window > 0) span = std::min<int64_t>(span, (int64_t)window + 16 * p.nt / group + 1);
+  span += kBlock - 1;   // a range may start up to 31 tokens before its first visible one
+  const int64_t base = (int64_t)batch * heads * p.tiles;
+  constexpr int64_t kStep = kBlock * kWaves;   // one step of every wave
+  constexpr int64_t kTarget = 2048;            // workgroups that fill the chip several times
+  int64_t splits = std::max<int64_t>(1, std::min<int64_t>(kTarget / base, (span + kStep - 1) / kStep));
+  splits = std::min<int64_t>(splits, 256);
+  const int64_t chunk = ((span + splits - 1) / splits + kStep - 1) / kStep * kStep;
+  p.splits = (int)((span + chunk - 1) / chunk);
+  p.chunk = (int)chunk;
+  if (p.splits > 1)
+    p.ws_bytes = (size_t)p.splits * (size_t)rows * (size_t)heads_q * (size_t)(dim + 1) * sizeof(float);
+  return p;
+}
+
+hipError_t launch_kv_attention(KvAttnArgs a, bool e4m3, const KvAttnPlan &plan, void *ws,
+                               hipStream_t st) {
+  a.splits = plan.splits;
+  a.chunk = plan.chunk;
+  a.tiles = plan.tiles;
+  a.part_o = static_cast<float *>(ws);
+  a.part_lse = plan.splits > 1
+                   ? a.part_o + (size_t)plan.splits * a.s.rows * a.heads_q * a.c.dim
+                   : nullptr;
+  switch (a.c.dim) {
+    case 64: return launch_dim<64>(a, e4m3, plan.nt, st);
+    case 128: return launch_dim<128>(a, e4m3, plan.nt, st);
+    default: return launch_dim<256>(a, e4m3, plan.nt, st);
+  }
+}
+
+}  // namespace slq
