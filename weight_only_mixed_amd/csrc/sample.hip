@@ -6,12 +6,24 @@
 // filled with atomics and partial sums taken in any order without changing a
 // result, and a cut falls where the 64-bit definition puts it.
 //
-// One workgroup per row.  The three cuts are prefixes of one order (logit
-// descending, index ascending), so the kept set is "key above tau, or equal to
-// tau and among the first ties by index", with w >= min_p on top.  tau comes
-// from a radix descent over the 32-bit ordered keys with a (count, mass)
-// histogram per digit; the draw descends over index segments, one per wave.
+// The three cuts are prefixes of one order (logit descending, index
+// ascending).  Two launches:
+//  1. sample_units_kernel streams the logits once.  Each wave takes one unit of
+//     1024 * U consecutive elements and leaves a list of all its elements above
+//     a bound that rises as the unit goes by (about the unit's 16 or 32 largest),
+//     its best element, and where the row's settings need it the unit's mass.
+//  2. sample_pick_kernel, one workgroup per row, sorts the listed elements above
+//     the largest of the row's bounds (everything above it is listed): a sorted
+//     prefix of the row, usually hundreds of elements long.  A kept set that
+//     ends inside it is cut there and drawn from.  Without any cut the units'
+//     masses name the unit, and only that is read again.  A kept set that ends
+//     outside (a wide nucleus, thousands of ties) is found by a radix descent
+//     over the 32-bit ordered keys of the row with a (count, mass) histogram
+//     per digit, and drawn by a descent over index segments.
+// A row of at most kList elements needs no first launch: it is sorted whole.
 #include <float.h>
+
+#include <algorithm>
 
 #include "serve.h"
 #include "slq_device.h"
@@ -19,19 +31,91 @@
 namespace slq {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 1024;           // sample_pick_kernel
 constexpr int kWaves = kThreads / kWave;
 constexpr int kBins = 2048;
+constexpr int kUnitThreads = 256;        // sample_units_kernel: four units
+constexpr int kBatch = 1024;             // elements of a wave's step, 16 per lane
+constexpr int kCand = 128;               // list entries of a unit
+constexpr int kList = 2048;              // sorted entries of a row
+constexpr uint32_t kKeyNegInf = 0x007FFFFFu;   // key_of(-inf): the smallest key
+
+struct Unit {
+  uint64_t best;     // (key, ~index): the largest element, its lowest index
+  double mass;       // sum of exp((l - ref) / T), where the row needs it
+  float ref;
+  uint32_t bound;    // every element with a key above it is listed
+  uint32_t count;
+  uint32_t pad;
+};
 
 template <int T>
-__device__ __forceinline__ float load_logit(const void *row, int64_t i) {
-  float v;
-  if constexpr (T == kElemF32) v = static_cast<const float *>(row)[i];
-  else if constexpr (T == kElemBf16)
-    v = __builtin_bit_cast(float, (uint32_t) static_cast<const uint16_t *>(row)[i] << 16);
-  else v = (float)static_cast<const _Float16 *>(row)[i];
-  return fminf(v == v ? v : -INFINITY, FLT_MAX);   // NaN -> -inf, +inf -> finite
-}
+struct Logit;
+template <>
+struct Logit<kElemF32> {
+  typedef float4 Vec;
+  static constexpr int kBytes = 4, kPer = 4;
+  static __device__ __forceinline__ float get(Vec v, int i) { return (&v.x)[i]; }
+  static __device__ __forceinline__ float one(const char *p) { return *reinterpret_cast<const float *>(p); }
+};
+template <>
+struct Logit<kElemBf16> {
+  typedef u32x4_t Vec;
+  static constexpr int kBytes = 2, kPer = 8;
+  static __device__ __forceinline__ float get(Vec v, int i) {
+    return __builtin_bit_cast(float, i & 1 ? v[i >> 1] & 0xFFFF0000u : v[i >> 1] << 16);
+  }
+  static __device__ __forceinline__ float one(const char *p) {
+    return __builtin_bit_cast(float, (uint32_t) * reinterpret_cast<const uint16_t *>(p) << 16);
+  }
+};
+template <>
+struct Logit<kElemF16> {
+  typedef u32x4_t Vec;
+  static constexpr int kBytes = 2, kPer = 8;
+  static __device__ __forceinline__ float get(Vec v, int i) {
+    return f16_bits_to_f32(i & 1 ? v[i >> 1] >> 16 : v[i >> 1] & 0xFFFFu);
+  }
+  static __device__ __forceinline__ float one(const char *p) {
+    return (float)*reinterpret_cast<const _Float16 *>(p);
+  }
+};
+
+// NaN -> -inf, +inf -> the largest finite value.
+__device__ __forceinline__ float tame(float v) { return fminf(v == v ? v : -INFINITY, FLT_MAX); }
+
+// A row of logits as 16-byte vectors: slot i of the window is element i -
+// `skip`, the window starting at the 16-byte boundary at or before the row.
+// Vectors that stick out of the row are read element by element, so nothing
+// outside it is touched; slots outside it read as -inf.
+template <int T>
+struct Row {
+  const char *base;   // the boundary
+  int skip;           // slots before element 0
+  int64_t end;        // slot behind the last element
+  __device__ __forceinline__ Row(const SampleArgs &a, int64_t r) {
+    const char *p = static_cast<const char *>(a.logits) + r * a.row_stride * Logit<T>::kBytes;
+    skip = (int)((uintptr_t)p & 15) / Logit<T>::kBytes;
+    base = p - skip * Logit<T>::kBytes;
+    end = a.vocab + skip;
+  }
+  __device__ __forceinline__ float at(int64_t slot) const {
+    return slot >= skip && slot < end ? tame(Logit<T>::one(base + slot * Logit<T>::kBytes)) : -INFINITY;
+  }
+  // kPer slots from `slot`, a multiple of kPer
+  __device__ __forceinline__ void load(int64_t slot, float *v) const {
+    constexpr int P = Logit<T>::kPer;
+    if (slot >= skip && slot + P <= end) {
+      const typename Logit<T>::Vec w =
+          *reinterpret_cast<const typename Logit<T>::Vec *>(base + slot * Logit<T>::kBytes);
+#pragma unroll
+      for (int i = 0; i < P; ++i) v[i] = tame(Logit<T>::get(w, i));
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i) v[i] = at(slot + i);
+    }
+  }
+};
 
 // Order-preserving 32-bit key (-0 and +0 are equal logits).
 __device__ __forceinline__ uint32_t key_of(float v) {
@@ -86,16 +170,214 @@ __device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
   return v;
 }
 
-struct Shared {
-  uint32_t count[kBins];
-  unsigned long long mass[kBins];
-  uint64_t a[kWaves], b[kWaves];
-  uint32_t digit;
-  uint64_t above_n, above_m;
+
+// A row's settings.
+struct Cuts {
+  float temp;
+  int64_t k;       // vocab: no limit
+  double p;        // 1: all
+  double min_w;    // 0: all
+  __device__ __forceinline__ Cuts(const SampleArgs &a, int64_t r) {
+    temp = a.temperature ? a.temperature[r] : 1.f;
+    const int64_t kk = a.top_k ? a.top_k[r] : 0;
+    k = kk > 0 && kk < a.vocab ? kk : a.vocab;
+    const float pp = a.top_p ? a.top_p[r] : 1.f, m = a.min_p ? a.min_p[r] : 0.f;
+    p = pp < 1.f ? (double)pp : 1.0;
+    min_w = m > 0.f ? fmin((double)m, 1.0) : 0.0;
+  }
+  __device__ __forceinline__ bool greedy() const { return !(temp > 0.f); }
+  // whether the mass of the whole row is asked for
+  __device__ __forceinline__ bool row_mass(int64_t vocab) const {
+    return !greedy() && k == vocab && (p < 1.0 || min_w == 0.0);
+  }
 };
 
-// The elements strictly above key tau number `above_n` and weigh `above_m`;
-// `ties` elements equal it.
+// The n-th largest of the wave's keys, n <= their number.
+template <int PER>
+__device__ uint32_t wave_nth(const uint32_t (&key)[PER], int n) {
+  uint32_t t = 0;
+  for (int b = 31; b >= 0; --b) {
+    const uint32_t c = t | 1u << b;
+    int have = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) have += __popcll(__ballot(key[i] >= c));
+    if (have >= n) t = c;
+  }
+  return t;
+}
+
+template <int T>
+__global__ __launch_bounds__(kUnitThreads) void sample_units_kernel(SampleArgs a, Unit *units,
+                                                                    uint64_t *lists, int per_row,
+                                                                    int steps, int keep) {
+  __shared__ uint64_t lds[kUnitThreads / kWave][kCand];
+  constexpr int P = Logit<T>::kPer, V = 16 / P;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  uint64_t *list = lds[wave];
+  const uint64_t below = (1ull << lane) - 1;
+  const int groups = (per_row + kUnitThreads / kWave - 1) / (kUnitThreads / kWave);
+  for (int64_t task = blockIdx.x; task < a.rows * groups; task += gridDim.x) {
+    const int64_t r = task / groups;
+    const int unit = (int)(task % groups) * (kUnitThreads / kWave) + wave;
+    if (unit >= per_row) continue;
+    const Row<T> row(a, r);
+    const Cuts cuts(a, r);
+    const bool with_mass = cuts.row_mass(a.vocab);
+    const double inv_t = 1.0 / (double)cuts.temp;
+    const int64_t beg = (int64_t)unit * steps * kBatch;
+    uint32_t bound = kKeyNegInf;
+    int n = 0;
+    uint64_t best = 0;
+    double mass = 0.0;
+    float ref = -INFINITY;
+    float next[16];
+#pragma unroll
+    for (int j = 0; j < V; ++j) row.load(beg + (j * kWave + lane) * P, next + j * P);
+    for (int s = 0; s < steps; ++s) {
+      const int64_t at = beg + (int64_t)s * kBatch;
+      if (at >= row.end) break;
+      float v[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = next[e];
+      if (s + 1 < steps) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) row.load(at + kBatch + (j * kWave + lane) * P, next + j * P);
+      }
+      float mx = v[0];
+#pragma unroll
+      for (int e = 1; e < 16; ++e) mx = fmaxf(mx, v[e]);
+      const uint32_t kmax = key_of(mx);
+      if (s == 0) {
+        // `keep` distinct elements are at least the keep-th largest lane maximum
+        const uint32_t one[1] = {kmax};
+        if (__popcll(__ballot(kmax > kKeyNegInf)) >= keep) bound = wave_nth(one, keep) - 1;
+      }
+      if (with_mass) {
+        const float top = wave_max(mx);
+        if (top > ref) {
+          if (ref != -INFINITY) mass *= exp_neg(((double)ref - (double)top) * inv_t);
+          ref = top;
+        }
+        if (ref != -INFINITY) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            mass += v[e] == -INFINITY ? 0.0 : exp_neg(((double)v[e] - (double)ref) * inv_t);
+        }
+      }
+      if ((uint32_t)(best >> 32) < kmax) {   // per lane: its own lowest index of a new largest
+#pragma unroll
+        for (int e = 15; e >= 0; --e)
+          if (v[e] == mx) {
+            const int64_t i = at + ((e / P) * kWave + lane) * P + e % P - row.skip;
+            best = (uint64_t)kmax << 32 | (uint32_t)~(uint32_t)i;
+          }
+      }
+      if (!__any(kmax > bound)) continue;
+      uint32_t key[16];
+      int more = 0;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        key[e] = key_of(v[e]);
+        more += __popcll(__ballot(key[e] > bound));
+      }
+      if (n + more > kCand) {
+        // too many: the bound moves to the keep-th largest of list and batch
+        uint32_t all[18];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) all[e] = key[e];
+        uint64_t old[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          old[e] = e * kWave + lane < n ? list[e * kWave + lane] : 0;
+          all[16 + e] = (uint32_t)(old[e] >> 32);
+        }
+        bound = wave_nth(all, keep);
+        n = 0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bool in = all[16 + e] > bound;
+          const uint64_t m = __ballot(in);
+          if (in) list[n + __popcll(m & below)] = old[e];
+          n += __popcll(m);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const bool in = key[e] > bound;
+        const uint64_t m = __ballot(in);
+        if (m) {
+          if (in) {
+            const int64_t i = at + ((e / P) * kWave + lane) * P + e % P - row.skip;
+            list[n + __popcll(m & below)] = (uint64_t)key[e] << 32 | (uint32_t)~(uint32_t)i;
+          }
+          n += __popcll(m);
+        }
+      }
+    }
+    best = wave_max_u64(best);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) mass += __shfl_xor(mass, o, kWave);
+    const int64_t slot = r * per_row + unit;
+    if (lane == 0) units[slot] = Unit{best, mass, ref, bound, (uint32_t)n, 0u};
+    for (int e = lane; e < n; e += kWave) lists[slot * kCand + e] = list[e];
+  }
+}
+
+struct Shared {
+  union {
+    struct {
+      uint32_t count[kBins];
+      unsigned long long mass[kBins];
+    } hist;
+    struct {
+      uint64_t entry[kList];          // sorted: (key, ~index) descending
+      unsigned long long mass[kList];
+      uint64_t order[kList];
+    } list;
+  };
+  uint64_t a[kWaves], b[kWaves];
+  double d[kWaves];
+  uint32_t digit, listed;
+  uint64_t above_n, above_m;
+  int64_t pos;
+};
+
+__device__ __forceinline__ uint64_t block_max_u64(uint64_t v, Shared &sh) {
+  v = wave_max_u64(v);
+  __syncthreads();
+  if ((threadIdx.x & (kWave - 1)) == 0) sh.a[threadIdx.x / kWave] = v;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) v = sh.a[w] > v ? sh.a[w] : v;
+  return v;
+}
+
+// Descending bitonic sort of n (a power of two, 64 .. kList) words.  Exchanges
+// of distance <= 64 stay within the 128 words that one wave's 64 pairs cover.
+__device__ void block_sort(uint64_t *x, int n) {
+  int before = kList;   // distance of the previous step
+  for (int k = 2; k <= n; k <<= 1)
+    for (int j = k >> 1; j >= 1; j >>= 1) {
+      if (j > kWave || before > kWave) __syncthreads();
+      else __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      before = j;
+      const int p = threadIdx.x;
+      if (p < n / 2) {
+        const int lo = 2 * p - (p & (j - 1)), hi = lo + j;
+        const uint64_t u = x[lo], w = x[hi];
+        if ((u < w) == ((lo & k) == 0)) {
+          x[lo] = w;
+          x[hi] = u;
+        }
+      }
+    }
+  __syncthreads();
+}
+
+// The elements strictly above key tau number `above_n` and weigh `above_m`
+// (0 without masses); `ties` elements equal it.
 struct Cut {
   uint32_t tau;
   uint64_t above_n, above_m, ties;
@@ -105,28 +387,34 @@ struct Cut {
 // false) or the running mass reaches `want_m` (by_mass true).  Every thread
 // returns the same cut.  The wanted amount is at most the total.
 template <int T>
-__device__ Cut descend(const void *row, int64_t vocab, const Weigh &wg, bool by_mass,
+__device__ Cut descend(const Row<T> &row, const Weigh &wg, bool by_mass, bool with_mass,
                        uint64_t want_n, double want_m, Shared &sh) {
+  constexpr int P = Logit<T>::kPer;
   uint32_t prefix = 0;
   uint64_t above_n = 0, above_m = 0, ties = 0;
   int shift = 32;
-  const int bits[3] = {11, 11, 10};
-#pragma unroll
   for (int level = 0; level < 3; ++level) {
-    const int next = shift - bits[level];
-    const uint32_t bins = 1u << bits[level];
+    const int bits = level < 2 ? 11 : 10;
+    const int next = shift - bits;
+    const uint32_t bins = 1u << bits;
+    __syncthreads();
     for (uint32_t i = threadIdx.x; i < bins; i += kThreads) {
-      sh.count[i] = 0;
-      sh.mass[i] = 0;
+      sh.hist.count[i] = 0;
+      sh.hist.mass[i] = 0;
     }
     __syncthreads();
-    for (int64_t i = threadIdx.x; i < vocab; i += kThreads) {
-      const float v = load_logit<T>(row, i);
-      const uint32_t k = key_of(v);
-      if (level == 0 || k >> shift == prefix) {
-        const uint32_t d = (k >> next) & (bins - 1);
-        atomicAdd(&sh.count[d], 1u);
-        atomicAdd(&sh.mass[d], (unsigned long long)wg.mass(wg.weight(v)));
+#pragma unroll 2
+    for (int64_t s = (int64_t)threadIdx.x * P; s < row.end; s += kThreads * P) {
+      float v[P];
+      row.load(s, v);
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        const uint32_t k = key_of(v[e]);
+        if (k > kKeyNegInf && (level == 0 || k >> shift == prefix)) {
+          const uint32_t d = (k >> next) & (bins - 1);
+          atomicAdd(&sh.hist.count[d], 1u);
+          if (with_mass) atomicAdd(&sh.hist.mass[d], (unsigned long long)wg.mass(wg.weight(v[e])));
+        }
       }
     }
     __syncthreads();
@@ -135,7 +423,8 @@ __device__ Cut descend(const void *row, int64_t vocab, const Weigh &wg, bool by_
       bool done = false;
       for (int base = (int)bins - kWave; base >= 0 && !done; base -= kWave) {
         const int d = base + kWave - 1 - lane;
-        uint64_t n = sh.count[d], m = sh.mass[d];
+        uint64_t n = sh.hist.count[d], m = sh.hist.mass[d];
+        if (!__any(n > 0)) continue;
         const uint64_t n0 = n, m0 = m;
 #pragma unroll
         for (int o = 1; o < kWave; o <<= 1) {
@@ -163,118 +452,65 @@ __device__ Cut descend(const void *row, int64_t vocab, const Weigh &wg, bool by_
       }
       if (!done && lane == 0) {   // rounding put the wanted mass behind the last element
         uint32_t d = 0;
-        while (d + 1 < bins && sh.count[d] == 0) ++d;
+        while (d + 1 < bins && sh.hist.count[d] == 0) ++d;
         sh.digit = d;
-        sh.above_n = above_n - sh.count[d];
-        sh.above_m = above_m - sh.mass[d];
+        sh.above_n = above_n - sh.hist.count[d];
+        sh.above_m = above_m - sh.hist.mass[d];
       }
     }
     __syncthreads();
     const uint32_t d = sh.digit;
     above_n = sh.above_n;
     above_m = sh.above_m;
-    ties = sh.count[d];
-    prefix = level == 0 ? d : prefix << bits[level] | d;
+    ties = sh.hist.count[d];
+    prefix = level == 0 ? d : prefix << bits | d;
     shift = next;
-    __syncthreads();
   }
   return Cut{prefix, above_n, above_m, ties};
 }
 
+// Draws from the elements with key > tau and the first `quota` ones equal to
+// it, of weight >= min_w, among slots [beg, end): a descent over index
+// segments, one per wave, to the 64 slots that hold the answer.  `target` < 0:
+// u times the mass found (the range is the whole row); else the mass that the
+// range's elements must exceed.  `total`: the mass that the token's share is
+// taken of (0: the mass found).
 template <int T>
-__global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a) {
-  __shared__ Shared sh;
-  const int64_t r = blockIdx.x;
+__device__ void draw(const SampleArgs &a, int64_t r, const Row<T> &row, const Weigh &wg,
+                     uint32_t tau, uint64_t quota, double min_w, int64_t beg, int64_t end,
+                     double target, double total, Shared &sh) {
+  constexpr int P = Logit<T>::kPer;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const void *row = static_cast<const char *>(a.logits) + r * a.row_stride * (T == kElemF32 ? 4 : 2);
-
-  uint64_t best = 0;   // (key, ~index): the largest logit, its lowest index
-  for (int64_t i = threadIdx.x; i < a.vocab; i += kThreads) {
-    const uint64_t k = (uint64_t)key_of(load_logit<T>(row, i)) << 32 | (uint32_t)~(uint32_t)i;
-    best = k > best ? k : best;
-  }
-  best = wave_max_u64(best);
-  if (lane == 0) sh.a[wave] = best;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) best = sh.a[w] > best ? sh.a[w] : best;
-  __syncthreads();
-  const float top = value_of((uint32_t)(best >> 32));
-  const float temp = a.temperature ? a.temperature[r] : 1.f;
-  if (top == -INFINITY || !(temp > 0.f)) {
-    if (threadIdx.x == 0) {
-      a.tokens[r] = top == -INFINITY ? -1 : (int32_t)~(uint32_t)best;
-      if (a.logprobs) a.logprobs[r] = top == -INFINITY ? -INFINITY : 0.f;
+  const double wt = wg.weight(value_of(tau));
+  const uint64_t w_tau = wt >= min_w ? wg.mass(wt) : 0;
+  uint64_t ties_before = 0, mass_before = 0;
+  auto take = [&](float v, uint64_t &m, uint64_t &t) {
+    const uint32_t k = key_of(v);
+    if (k > tau) {
+      const double w = wg.weight(v);
+      m += w >= min_w ? wg.mass(w) : 0;
+    } else if (k == tau) {
+      ++t;
     }
-    return;
-  }
-  const int s = 62 - (a.vocab > 1 ? 64 - __builtin_clzll((uint64_t)a.vocab - 1) : 0);
-  const Weigh wg{(double)top, 1.0 / (double)temp, ldexp(1.0, s)};
-  const int64_t k = a.top_k ? a.top_k[r] : 0;
-  const float p = a.top_p ? a.top_p[r] : 1.f;
-  const float mp = a.min_p ? a.min_p[r] : 0.f;
-  const double min_w = mp > 0.f ? fmin((double)mp, 1.0) : 0.0;
-
-  uint32_t tau = 0;                 // kept: key > tau, or == tau and among the first `quota` ties
-  uint64_t quota = (uint64_t)a.vocab;
-  double of_mass = -1.0;            // mass that top_p refers to
-  if (k > 0 && k < a.vocab) {
-    const Cut c = descend<T>(row, a.vocab, wg, false, (uint64_t)k, 0.0, sh);
-    tau = c.tau;
-    quota = (uint64_t)k - c.above_n;
-    of_mass = (double)(c.above_m + quota * wg.mass(wg.weight(value_of(tau))));
-  }
-  if (p < 1.f) {
-    if (of_mass < 0.0) {
-      uint64_t m = 0;
-      for (int64_t i = threadIdx.x; i < a.vocab; i += kThreads)
-        m += wg.mass(wg.weight(load_logit<T>(row, i)));
-      m = wave_sum_u64(m);
-      if (lane == 0) sh.a[wave] = m;
-      __syncthreads();
-      m = 0;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) m += sh.a[w];
-      __syncthreads();
-      of_mass = (double)m;
-    }
-    // shortest prefix with mass >= p * of_mass; at least one token
-    const double want = fmax((double)p * of_mass, 1.0);
-    const Cut c = descend<T>(row, a.vocab, wg, true, 0, want, sh);
-    const uint64_t w = wg.mass(wg.weight(value_of(c.tau)));
-    const double need = want - (double)c.above_m;
-    uint64_t q = w > 0 ? (uint64_t)ceil(need / (double)w) : c.ties;
-    if (q < 1) q = 1;
-    if (q > c.ties) q = c.ties;
-    if (c.tau > tau) {
-      tau = c.tau;
-      quota = q;
-    } else if (c.tau == tau && q < quota) {
-      quota = q;
-    }
-  }
-
-  // draw: descend over index segments, one per wave
-  int64_t beg = 0, end = a.vocab;
-  const uint64_t w_tau = [&] {
-    const double w = wg.weight(value_of(tau));
-    return w >= min_w ? wg.mass(w) : 0;
-  }();
-  uint64_t ties_before = 0, mass_before = 0, total = 0;
-  double target = 0.0;
-  for (bool first = true;; first = false) {
-    const int64_t seg = (((end - beg + kWaves - 1) / kWaves) + kWave - 1) / kWave * kWave;
+  };
+  do {
+    const int64_t len = end - beg;
+    const bool wide = len > kWave * kWaves;   // whole vectors per lane
+    const int64_t grain = wide ? kWave * P : kWave;
+    const int64_t seg = ((len + kWaves - 1) / kWaves + grain - 1) / grain * grain;
     const int64_t s0 = min(beg + seg * wave, end), s1 = min(s0 + seg, end);
     uint64_t m = 0, t = 0;
-    for (int64_t i = s0 + lane; i < s1; i += kWave) {
-      const float v = load_logit<T>(row, i);
-      const uint32_t kk = key_of(v);
-      if (kk > tau) {
-        const double w = wg.weight(v);
-        m += w >= min_w ? wg.mass(w) : 0;
-      } else if (kk == tau) {
-        ++t;
+    if (wide) {
+#pragma unroll 2
+      for (int64_t s = s0 + lane * P; s < s1; s += kWave * P) {
+        float v[P];
+        row.load(s, v);
+#pragma unroll
+        for (int e = 0; e < P; ++e)
+          if (s + e < s1) take(v[e], m, t);
       }
+    } else {
+      for (int64_t s = s0 + lane; s < s1; s += kWave) take(row.at(s), m, t);
     }
     m = wave_sum_u64(m);
     t = wave_sum_u64(t);
@@ -289,19 +525,18 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a) {
       const uint64_t left = quota > before ? quota - before : 0;
       return sh.a[w] + (sh.b[w] < left ? sh.b[w] : left) * w_tau;
     };
-    if (first) {
-      uint64_t tb = 0;
+    if (target < 0.0) {
+      uint64_t tb = 0, sum = 0;
       for (int w = 0; w < kWaves; ++w) {
-        total += seg_mass(w, tb);
+        sum += seg_mass(w, tb);
         tb += sh.b[w];
       }
       const float u = a.u[r];
-      target = fmin((double)(u > 0.f ? u : 0.f) * (double)total, (double)(total - 1));
+      target = fmin((double)(u > 0.f ? u : 0.f) * (double)sum, (double)(sum - 1));
+      if (total == 0.0) total = (double)sum;
     }
-    int pick = -1;
-    uint64_t tb = ties_before, mb = mass_before;
-    int last = 0;
-    uint64_t last_tb = tb, last_mb = mb;
+    int pick = -1, last = 0;
+    uint64_t tb = ties_before, mb = mass_before, last_tb = tb, last_mb = mb;
     for (int w = 0; w < kWaves; ++w) {
       const uint64_t sm = seg_mass(w, tb);
       if (sm > 0) {
@@ -316,61 +551,371 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a) {
       mb += sm;
       tb += sh.b[w];
     }
-    if (pick < 0) {
-      pick = last;
-      tb = last_tb;
-      mb = last_mb;
-    }
-    ties_before = tb;
-    mass_before = mb;
-    const int64_t n0 = min(beg + seg * pick, end);
+    ties_before = pick < 0 ? last_tb : tb;
+    mass_before = pick < 0 ? last_mb : mb;
+    const int64_t n0 = min(beg + seg * (pick < 0 ? last : pick), end);
     end = min(n0 + seg, end);
     beg = n0;
-    if (end - beg <= kWave) break;
-  }
+  } while (end - beg > kWave);
   if (wave == 0) {
-    const int64_t i = beg + lane;
-    uint64_t m = 0;
-    bool tie = false;
-    float v = -INFINITY;
-    if (i < end) {
-      v = load_logit<T>(row, i);
-      const uint32_t kk = key_of(v);
-      tie = kk == tau;
-      if (kk > tau) {
-        const double w = wg.weight(v);
-        m = w >= min_w ? wg.mass(w) : 0;
-      }
-    }
-    const uint64_t tm = __ballot(tie);
-    if (tie && ties_before + __popcll(tm & ((1ull << lane) - 1)) < quota) m = w_tau;
+    const int64_t slot = beg + lane;
+    const float v = slot < end ? row.at(slot) : -INFINITY;
+    uint64_t m = 0, t = 0;
+    if (slot < end) take(v, m, t);
+    const uint64_t tm = __ballot(t > 0);
+    if (t > 0 && ties_before + __popcll(tm & ((1ull << lane) - 1)) < quota) m = w_tau;
     uint64_t c = m;
 #pragma unroll
     for (int o = 1; o < kWave; o <<= 1) {
-      const uint64_t t = __shfl_up((unsigned long long)c, o, kWave);
-      if (lane >= o) c += t;
+      const uint64_t up = __shfl_up((unsigned long long)c, o, kWave);
+      if (lane >= o) c += up;
     }
-    uint64_t hit = __ballot(m > 0 && (double)(mass_before + c) > target);
+    const uint64_t hit = __ballot(m > 0 && (double)(mass_before + c) > target);
     const uint64_t some = __ballot(m > 0);
     const int who = hit ? __builtin_ctzll(hit) : 63 - __builtin_clzll(some | 1ull);
     if (lane == who) {
-      a.tokens[r] = (int32_t)i;
+      a.tokens[r] = (int32_t)(slot - row.skip);
       if (a.logprobs)
-        a.logprobs[r] = (float)(((double)v - wg.max) * wg.inv_t - log((double)total / wg.unit));
+        a.logprobs[r] = (float)(((double)v - wg.max) * wg.inv_t - log(total / wg.unit));
     }
   }
 }
 
+// The first n entries of the sorted list are kept: draw from them by index.
+__device__ void draw_listed(const SampleArgs &a, int64_t r, const Weigh &wg, int n, Shared &sh) {
+  int size = kWave;
+  while (size < n) size <<= 1;
+  for (int i = threadIdx.x; i < size; i += kThreads)   // ~index descending: index ascending
+    sh.list.order[i] = i < n ? (sh.list.entry[i] & 0xFFFFFFFFull) << 32 | (uint32_t)i : 0;
+  block_sort(sh.list.order, size);
+  // each thread two neighbours, a scan over threads
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int i0 = 2 * threadIdx.x;
+  uint64_t m[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    m[e] = i0 + e < n ? sh.list.mass[(uint32_t)sh.list.order[i0 + e]] : 0;
+  uint64_t c = m[0] + m[1];
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const uint64_t up = __shfl_up((unsigned long long)c, o, kWave);
+    if (lane >= o) c += up;
+  }
+  __syncthreads();
+  if (lane == kWave - 1) sh.a[wave] = c;
+  __syncthreads();
+  uint64_t total = 0, mine = 0;
+  for (int w = 0; w < kWaves; ++w) {
+    if (w == wave) mine = total;
+    total += sh.a[w];
+  }
+  c += mine;
+  const float u = a.u[r];
+  const double target = fmin((double)(u > 0.f ? u : 0.f) * (double)total, (double)(total - 1));
+  const uint64_t c1 = c, c0 = c - m[1];   // running mass through each neighbour
+  // the last entry with any mass, where rounding puts the target at the total
+  if (m[0] > 0 && c0 == total) sh.pos = i0;
+  if (m[1] > 0 && c1 == total) sh.pos = i0 + 1;
+  __syncthreads();
+  if (m[0] > 0 && (double)c0 > target && !((double)(c0 - m[0]) > target)) sh.pos = i0;
+  else if (m[1] > 0 && (double)c1 > target && !((double)(c1 - m[1]) > target)) sh.pos = i0 + 1;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const uint64_t e = sh.list.entry[(uint32_t)sh.list.order[sh.pos]];
+    a.tokens[r] = (int32_t)~(uint32_t)e;
+    if (a.logprobs)
+      a.logprobs[r] = (float)(((double)value_of((uint32_t)(e >> 32)) - wg.max) * wg.inv_t -
+                              log((double)total / wg.unit));
+  }
+}
+
+// per_row = 0: the row is listed whole, no units.
+template <int T>
+__global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, const Unit *units,
+                                                               const uint64_t *lists, int per_row,
+                                                               int steps) {
+  __shared__ Shared sh;
+  constexpr int P = Logit<T>::kPer;
+  const int64_t r = blockIdx.x;
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const Row<T> row(a, r);
+  const Cuts cuts(a, r);
+  units += r * per_row;
+  lists += r * per_row * kCand;
+
+  // the largest logit and the bound above which every element is listed
+  uint64_t best = 0;
+  uint32_t bound = kKeyNegInf;
+  if (threadIdx.x == 0) sh.listed = 0;
+  if (per_row == 0) {
+    __syncthreads();
+    for (int64_t s = (int64_t)threadIdx.x * P; s < row.end; s += kThreads * P) {
+      float v[P];
+      row.load(s, v);
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        if (s + e < row.skip || s + e >= row.end) continue;
+        const uint32_t k = key_of(v[e]);
+        const uint64_t x = (uint64_t)k << 32 | (uint32_t)~(uint32_t)(s + e - row.skip);
+        best = x > best ? x : best;
+        if (k > kKeyNegInf) sh.list.entry[atomicAdd(&sh.listed, 1u)] = x;
+      }
+    }
+    best = block_max_u64(best, sh);
+  } else {
+    for (int i = threadIdx.x; i < per_row; i += kThreads) {
+      best = units[i].best > best ? units[i].best : best;
+      bound = max(bound, units[i].bound);
+    }
+    best = block_max_u64(best, sh);
+    bound = (uint32_t)block_max_u64(bound, sh);
+  }
+  const float top = value_of((uint32_t)(best >> 32));
+  if (top == -INFINITY || cuts.greedy()) {
+    if (threadIdx.x == 0) {
+      a.tokens[r] = top == -INFINITY ? -1 : (int32_t)~(uint32_t)best;
+      if (a.logprobs) a.logprobs[r] = top == -INFINITY ? -INFINITY : 0.f;
+    }
+    return;
+  }
+  const int s = 62 - (a.vocab > 1 ? 64 - __builtin_clzll((uint64_t)a.vocab - 1) : 0);
+  const Weigh wg{(double)top, 1.0 / (double)cuts.temp, ldexp(1.0, s)};
+
+  // the row's mass, in the order of the units
+  double row_mass = 0.0;
+  const bool free_draw = cuts.k == a.vocab && !(cuts.p < 1.0) && cuts.min_w == 0.0;
+  if (per_row > 0 && cuts.row_mass(a.vocab)) {
+    // thread w * 64 + l takes units l + 64 w + 1024 n ...: a fixed order
+    double m = 0.0;
+    for (int i = threadIdx.x; i < per_row; i += kThreads)
+      if (units[i].ref != -INFINITY) m += units[i].mass * wg.weight(units[i].ref);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) m += __shfl_xor(m, o, kWave);
+    __syncthreads();
+    if (lane == 0) sh.d[wave] = m;
+    __syncthreads();
+    for (int w = 0; w < kWaves; ++w) row_mass += sh.d[w];
+    row_mass *= wg.unit;
+  }
+
+  if (per_row > 0 && free_draw) {
+    // the unit that holds the draw: wave 0 scans the units' masses by index
+    const float u = a.u[r];
+    const double target = fmin((double)(u > 0.f ? u : 0.f), 1.0 - 0x1p-53) * row_mass;
+    if (wave == 0) {
+      double before = 0.0;
+      int64_t pick = -1, last = 0;
+      double pick_before = 0.0, last_before = 0.0;
+      for (int base = 0; base < per_row && pick < 0; base += kWave) {
+        const int i = base + lane;
+        const double m = i < per_row && units[i].ref != -INFINITY
+                             ? units[i].mass * wg.weight(units[i].ref) * wg.unit : 0.0;
+        double c = m;
+#pragma unroll
+        for (int o = 1; o < kWave; o <<= 1) {
+          const double up = __shfl_up(c, o, kWave);
+          if (lane >= o) c += up;
+        }
+        // (a unit of less mass than elements may hold no element of any)
+        const bool holds = m >= (double)steps * kBatch;
+        const uint64_t some = __ballot(holds);
+        const uint64_t hit = __ballot(holds && before + c > target);
+        if (hit) {
+          const int who = __builtin_ctzll(hit);
+          pick = base + who;
+          pick_before = before + __shfl(c - m, who, kWave);
+        } else if (some) {
+          const int who = 63 - __builtin_clzll(some);
+          last = base + who;
+          last_before = before + __shfl(c - m, who, kWave);
+        }
+        before += __shfl(c, kWave - 1, kWave);
+      }
+      if (lane == 0) {
+        sh.pos = pick < 0 ? last : pick;
+        sh.d[0] = pick < 0 ? last_before : pick_before;
+      }
+    }
+    __syncthreads();
+    const int64_t at = sh.pos;
+    const double rest = target - sh.d[0];
+    const int64_t unit = (int64_t)steps * kBatch;
+    __syncthreads();
+    draw<T>(a, r, row, wg, 0u, 0, 0.0, at * unit, min((at + 1) * unit, row.end),
+            rest > 0.0 ? rest : 0.0, row_mass, sh);
+    return;
+  }
+
+  // the listed elements above the bound, sorted
+  if (per_row > 0) {
+    __syncthreads();
+    for (int64_t i = threadIdx.x; i < (int64_t)per_row * kCand; i += kThreads) {
+      const int unit = (int)(i / kCand), e = (int)(i % kCand);
+      if (e < (int)units[unit].count) {
+        const uint64_t x = lists[i];
+        if ((uint32_t)(x >> 32) > bound) {
+          const uint32_t at = atomicAdd(&sh.listed, 1u);
+          if (at < kList) sh.list.entry[at] = x;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  const int listed = (int)sh.listed;
+  const bool whole = bound == kKeyNegInf && listed <= kList;   // every element above -inf
+  if (listed <= kList && listed > 0) {
+    int size = kWave;
+    while (size < listed) size <<= 1;
+    for (int i = listed + threadIdx.x; i < size; i += kThreads) sh.list.entry[i] = 0;
+    block_sort(sh.list.entry, size);
+    // masses, their running sum, and where each cut falls
+    const int i0 = 2 * threadIdx.x;
+    uint64_t m[2];
+    int heavy = 0;   // entries of weight >= min_w
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      m[e] = 0;
+      if (i0 + e < listed) {
+        const double w = wg.weight(value_of((uint32_t)(sh.list.entry[i0 + e] >> 32)));
+        m[e] = wg.mass(w);
+        sh.list.mass[i0 + e] = m[e];
+        heavy += w >= cuts.min_w;
+      }
+    }
+    uint64_t c = m[0] + m[1];
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const uint64_t up = __shfl_up((unsigned long long)c, o, kWave);
+      if (lane >= o) c += up;
+    }
+    const uint64_t hw = wave_sum_u64((uint64_t)heavy);
+    __syncthreads();
+    if (lane == kWave - 1) {
+      sh.a[wave] = c;
+      sh.b[wave] = hw;
+    }
+    __syncthreads();
+    uint64_t before = 0, all = 0, n_min = 0;
+    for (int w = 0; w < kWaves; ++w) {
+      if (w == wave) before = all;
+      all += sh.a[w];
+      n_min += sh.b[w];
+    }
+    const uint64_t run1 = before + c, run0 = run1 - m[1];   // running mass through i0, i0 + 1
+    const int64_t n_k = min<int64_t>(cuts.k, listed);
+    const bool k_inside = cuts.k <= listed || whole;
+    // mass that top_p refers to
+    if (i0 == n_k - 1) sh.above_m = run0;
+    if (i0 + 1 == n_k - 1) sh.above_m = run1;
+    if (threadIdx.x == 0) sh.pos = listed;
+    __syncthreads();
+    bool inside = k_inside;
+    int64_t n = n_k;
+    if (cuts.p < 1.0) {
+      const double of = k_inside ? (double)sh.above_m : row_mass;
+      const double want = fmax(cuts.p * of, 1.0);
+      // the first entry whose running mass reaches the wanted one
+      if (i0 < listed && (double)run0 >= want && !((double)(run0 - m[0]) >= want)) sh.pos = i0;
+      else if (i0 + 1 < listed && (double)run1 >= want && !((double)(run1 - m[1]) >= want))
+        sh.pos = i0 + 1;
+      __syncthreads();
+      const int64_t n_p = sh.pos < listed ? sh.pos + 1 : listed;
+      // without a top-k inside the list the nucleus, or min_p, has to end inside it
+      if (!k_inside)
+        inside = cuts.k == a.vocab && (sh.pos < listed || (int64_t)n_min < listed);
+      n = min(n, n_p);
+    } else if (!k_inside) {
+      inside = (int64_t)n_min < listed;   // min_p alone cuts the list
+    }
+    if (cuts.min_w > 0.0) n = min<int64_t>(n, (int64_t)n_min);
+    if (inside) {
+      __syncthreads();
+      draw_listed(a, r, wg, (int)n, sh);
+      return;
+    }
+  }
+
+  // the kept set ends outside the list
+  uint32_t tau = 0;                 // kept: key > tau, or == tau and among the first `quota` ties
+  uint64_t quota = 0;
+  double of_mass = row_mass;
+  if (cuts.k < a.vocab) {
+    const bool with_mass = cuts.p < 1.0;
+    const Cut c = descend<T>(row, wg, false, with_mass, (uint64_t)cuts.k, 0.0, sh);
+    tau = c.tau;
+    quota = (uint64_t)cuts.k > c.above_n ? (uint64_t)cuts.k - c.above_n : 0;
+    const uint64_t ties = quota < c.ties ? quota : c.ties;
+    of_mass = (double)(c.above_m + ties * wg.mass(wg.weight(value_of(tau))));
+  }
+  if (cuts.p < 1.0) {
+    // shortest prefix with mass >= p * of_mass; at least one token
+    const double want = fmax(cuts.p * of_mass, 1.0);
+    const Cut c = descend<T>(row, wg, true, true, 0, want, sh);
+    const uint64_t w = wg.mass(wg.weight(value_of(c.tau)));
+    const double need = want - (double)c.above_m;
+    uint64_t q = w > 0 && need > 0.0 ? (uint64_t)ceil(need / (double)w) : w > 0 ? 1 : c.ties;
+    if (q < 1) q = 1;
+    if (q > c.ties) q = c.ties;
+    if (c.tau > tau) {
+      tau = c.tau;
+      quota = q;
+    } else if (c.tau == tau && q < quota) {
+      quota = q;
+    }
+  }
+  __syncthreads();
+  draw<T>(a, r, row, wg, tau, quota, cuts.min_w, 0, row.end, -1.0, 0.0, sh);
+}
+
+struct SamplePlan {
+  int per_row;   // units per row (0: rows short enough to be listed whole)
+  int steps;     // 1024-element steps per unit
+  int keep;
+};
+// Units of one step where rows are few (149 waves for one row of 151936), of
+// four where they are many: fewer, longer units list fewer elements per row.
+SamplePlan sample_plan(int64_t rows, int64_t vocab) {
+  SamplePlan p{0, 1, 16};
+  if (vocab <= kList) return p;
+  const int64_t slots = vocab + 7;   // a row may start up to 7 elements behind a boundary
+  int64_t steps = 1;
+  while (steps < 4 && rows * ((slots + steps * kBatch - 1) / (steps * kBatch)) > 8192) steps *= 2;
+  while ((slots + steps * kBatch - 1) / (steps * kBatch) > 4096) steps *= 2;
+  p.steps = (int)steps;
+  p.per_row = (int)((slots + steps * kBatch - 1) / (steps * kBatch));
+  p.keep = steps == 1 ? 16 : 32;
+  return p;
+}
+
+template <int T>
+hipError_t launch_type(const SampleArgs &a, void *ws, hipStream_t st) {
+  const SamplePlan p = sample_plan(a.rows, a.vocab);
+  const size_t n = (size_t)a.rows * p.per_row;
+  uint64_t *lists = static_cast<uint64_t *>(ws);
+  Unit *units = reinterpret_cast<Unit *>(lists + n * kCand);
+  if (p.per_row > 0) {
+    const int64_t tasks = a.rows * ((p.per_row + 3) / 4);
+    hipLaunchKernelGGL((sample_units_kernel<T>), dim3((unsigned)std::min<int64_t>(tasks, 1 << 20)),
+                       dim3(kUnitThreads), 0, st, a, units, lists, p.per_row, p.steps, p.keep);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((sample_pick_kernel<T>), dim3((unsigned)a.rows), dim3(kThreads), 0, st, a, units,
+                     lists, p.per_row, p.steps);
+  return hipGetLastError();
+}
+
 }  // namespace
 
-size_t sample_workspace(int64_t, int64_t) { return 0; }
+size_t sample_workspace(int64_t rows, int64_t vocab) {
+  const SamplePlan p = sample_plan(rows, vocab);
+  return (size_t)rows * p.per_row * (kCand * sizeof(uint64_t) + sizeof(Unit));
+}
 
-hipError_t launch_sample(const SampleArgs &a, int type, void *, hipStream_t st) {
-  const dim3 grid((unsigned)a.rows), block(kThreads);
-  if (type == kElemF32) hipLaunchKernelGGL((sample_row_kernel<kElemF32>), grid, block, 0, st, a);
-  else if (type == kElemBf16) hipLaunchKernelGGL((sample_row_kernel<kElemBf16>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((sample_row_kernel<kElemF16>), grid, block, 0, st, a);
-  return hipGetLastError();
+hipError_t launch_sample(const SampleArgs &a, int type, void *ws, hipStream_t st) {
+  if (type == kElemF32) return launch_type<kElemF32>(a, ws, st);
+  if (type == kElemBf16) return launch_type<kElemBf16>(a, ws, st);
+  return launch_type<kElemF16>(a, ws, st);
 }
 
 }  // namespace slq
