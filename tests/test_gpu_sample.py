@@ -118,6 +118,21 @@ def test_infinities_nan_and_empty_rows():
               top_k=np.full(10, -7, np.int32))
 
 
+def test_lists_that_end_at_zero():
+    """Units whose listed elements reach down to exactly +-0, and to the numbers beside it."""
+    g = np.random.default_rng(17)
+    l = -np.abs(g.standard_normal((6, 9000))).astype(np.float32)
+    for r in range(6):
+        at = g.permutation(9000)[:600]
+        l[r, at] = np.float32([0.0, -0.0, 1e-45, -1e-45, 0.0, 0.0])[r] * np.ones(600, np.float32)
+        l[r, at[:100]] = g.random(100)
+    u = g.random(6).astype(np.float32)
+    logits = torch.from_numpy(l).to(DEV)
+    for k in (20, 101, 350, 700):
+        check(logits, u, f"zeros top-k {k}", top_k=np.full(6, k, np.int32))
+    check(logits, u, "zeros top-p", top_p=np.float32([0.01, 0.05, 0.1, 0.12, 0.2, 0.5]))
+
+
 def test_strided_and_unaligned_rows():
     g = np.random.default_rng(3)
     wide = rows_of(g, 5, 5003, "bf16")

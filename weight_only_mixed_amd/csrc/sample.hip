@@ -53,15 +53,25 @@ template <int T>
 struct Logit;
 template <>
 struct Logit<kElemF32> {
-  typedef float4 Vec;
+  typedef f32x4_t Vec;
   static constexpr int kBytes = 4, kPer = 4;
-  static __device__ __forceinline__ float get(Vec v, int i) { return (&v.x)[i]; }
+  static constexpr float kNegInf = -INFINITY;
+  static __device__ __forceinline__ float get(Vec v, int i) { return v[i]; }
+  static __device__ __forceinline__ float bits(const char *p) { return *reinterpret_cast<const float *>(p); }
+  static __device__ __forceinline__ void set(Vec &v, int i, float x) { v[i] = x; }
   static __device__ __forceinline__ float one(const char *p) { return *reinterpret_cast<const float *>(p); }
 };
 template <>
 struct Logit<kElemBf16> {
   typedef u32x4_t Vec;
   static constexpr int kBytes = 2, kPer = 8;
+  static constexpr uint32_t kNegInf = 0xFF80u;
+  static __device__ __forceinline__ uint32_t bits(const char *p) {
+    return *reinterpret_cast<const uint16_t *>(p);
+  }
+  static __device__ __forceinline__ void set(Vec &v, int i, uint32_t x) {
+    v[i >> 1] = i & 1 ? v[i >> 1] | x << 16 : x;
+  }
   static __device__ __forceinline__ float get(Vec v, int i) {
     return __builtin_bit_cast(float, i & 1 ? v[i >> 1] & 0xFFFF0000u : v[i >> 1] << 16);
   }
@@ -73,6 +83,13 @@ template <>
 struct Logit<kElemF16> {
   typedef u32x4_t Vec;
   static constexpr int kBytes = 2, kPer = 8;
+  static constexpr uint32_t kNegInf = 0xFC00u;
+  static __device__ __forceinline__ uint32_t bits(const char *p) {
+    return *reinterpret_cast<const uint16_t *>(p);
+  }
+  static __device__ __forceinline__ void set(Vec &v, int i, uint32_t x) {
+    v[i >> 1] = i & 1 ? v[i >> 1] | x << 16 : x;
+  }
   static __device__ __forceinline__ float get(Vec v, int i) {
     return f16_bits_to_f32(i & 1 ? v[i >> 1] >> 16 : v[i >> 1] & 0xFFFFu);
   }
@@ -90,6 +107,7 @@ __device__ __forceinline__ float tame(float v) { return fminf(v == v ? v : -INFI
 // outside it is touched; slots outside it read as -inf.
 template <int T>
 struct Row {
+  typedef typename Logit<T>::Vec Vec;
   const char *base;   // the boundary
   int skip;           // slots before element 0
   int64_t end;        // slot behind the last element
@@ -102,17 +120,50 @@ struct Row {
   __device__ __forceinline__ float at(int64_t slot) const {
     return slot >= skip && slot < end ? tame(Logit<T>::one(base + slot * Logit<T>::kBytes)) : -INFINITY;
   }
-  // kPer slots from `slot`, a multiple of kPer
+  // whether slots [lo, hi) are all elements of the row
+  __device__ __forceinline__ bool inside(int64_t lo, int64_t hi) const { return lo >= skip && hi <= end; }
+  // kPer slots from `slot`, a multiple of kPer, wholly inside the row: one load,
+  // nothing done with it yet
+  __device__ __forceinline__ Vec raw(int64_t slot) const {
+    return *reinterpret_cast<const Vec *>(base + slot * Logit<T>::kBytes);
+  }
+  // the same anywhere
+  __device__ __forceinline__ Vec any(int64_t slot) const {
+    if (inside(slot, slot + Logit<T>::kPer)) return raw(slot);
+    Vec w;
+#pragma unroll
+    for (int i = 0; i < Logit<T>::kPer; ++i)
+      Logit<T>::set(w, i, slot + i >= skip && slot + i < end
+                              ? Logit<T>::bits(base + (slot + i) * Logit<T>::kBytes)
+                              : Logit<T>::kNegInf);
+    return w;
+  }
   __device__ __forceinline__ void load(int64_t slot, float *v) const {
+    const Vec w = any(slot);
+#pragma unroll
+    for (int i = 0; i < Logit<T>::kPer; ++i) v[i] = tame(Logit<T>::get(w, i));
+  }
+  // f(v, slot) for the kPer elements of each vector of slots first, first +
+  // step, ... below `stop` (<= end); kU loads in flight
+  template <int kU, typename F>
+  __device__ __forceinline__ void each(int64_t first, int64_t step, int64_t stop, F &&f) const {
     constexpr int P = Logit<T>::kPer;
-    if (slot >= skip && slot + P <= end) {
-      const typename Logit<T>::Vec w =
-          *reinterpret_cast<const typename Logit<T>::Vec *>(base + slot * Logit<T>::kBytes);
+    for (int64_t s = first; s < stop; s += kU * step) {
+      Vec w[kU];
+      // one branch for all: a load inside a divergent branch waits there
+      const bool in = __all(inside(s, s + (kU - 1) * step + P));
+      if (in) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) v[i] = tame(Logit<T>::get(w, i));
-    } else {
+        for (int u = 0; u < kU; ++u) w[u] = raw(s + u * step);
+      } else {
 #pragma unroll
-      for (int i = 0; i < P; ++i) v[i] = at(slot + i);
+        for (int u = 0; u < kU; ++u) w[u] = any(s + u * step);
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+          if (s + u * step + i < stop) f(tame(Logit<T>::get(w[u], i)), s + u * step + i);
     }
   }
 };
@@ -125,6 +176,10 @@ __device__ __forceinline__ uint32_t key_of(float v) {
 __device__ __forceinline__ float value_of(uint32_t k) {
   return __builtin_bit_cast(float, k ^ (k & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu));
 }
+
+// The float that v > limit compares with where key_of(v) > k is meant: +0 is the
+// key after that of -0, which no logit has.
+__device__ __forceinline__ float limit_of(uint32_t k) { return value_of(k == 0x7FFFFFFFu ? k - 1 : k); }
 
 // exp(x) for x <= 0 in fp64: x = n ln 2 + f, |f| <= ln 2 / 2, Taylor series of
 // degree 12 (remainder below 2e-16).  Below 2^-64 it is 0.
@@ -231,19 +286,24 @@ __global__ __launch_bounds__(kUnitThreads) void sample_units_kernel(SampleArgs a
     uint64_t best = 0;
     double mass = 0.0;
     float ref = -INFINITY;
-    float next[16];
+    typename Logit<T>::Vec next[V];
+    auto fetch = [&](int64_t at) {
+      if (row.inside(at, at + kBatch)) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) row.load(beg + (j * kWave + lane) * P, next + j * P);
+        for (int j = 0; j < V; ++j) next[j] = row.raw(at + (j * kWave + lane) * P);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) next[j] = row.any(at + (j * kWave + lane) * P);
+      }
+    };
+    fetch(beg);
     for (int s = 0; s < steps; ++s) {
       const int64_t at = beg + (int64_t)s * kBatch;
       if (at >= row.end) break;
       float v[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = next[e];
-      if (s + 1 < steps) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) row.load(at + kBatch + (j * kWave + lane) * P, next + j * P);
-      }
+      for (int e = 0; e < 16; ++e) v[e] = tame(Logit<T>::get(next[e / P], e % P));
+      if (s + 1 < steps) fetch(at + kBatch);
       float mx = v[0];
 #pragma unroll
       for (int e = 1; e < 16; ++e) mx = fmaxf(mx, v[e]);
@@ -274,18 +334,15 @@ __global__ __launch_bounds__(kUnitThreads) void sample_units_kernel(SampleArgs a
           }
       }
       if (!__any(kmax > bound)) continue;
-      uint32_t key[16];
+      float limit = limit_of(bound);   // v > limit: key above the bound
       int more = 0;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        key[e] = key_of(v[e]);
-        more += __popcll(__ballot(key[e] > bound));
-      }
+      for (int e = 0; e < 16; ++e) more += __popcll(__ballot(v[e] > limit));
       if (n + more > kCand) {
         // too many: the bound moves to the keep-th largest of list and batch
         uint32_t all[18];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) all[e] = key[e];
+        for (int e = 0; e < 16; ++e) all[e] = key_of(v[e]);
         uint64_t old[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -293,6 +350,7 @@ __global__ __launch_bounds__(kUnitThreads) void sample_units_kernel(SampleArgs a
           all[16 + e] = (uint32_t)(old[e] >> 32);
         }
         bound = wave_nth(all, keep);
+        limit = limit_of(bound);
         n = 0;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -304,12 +362,12 @@ __global__ __launch_bounds__(kUnitThreads) void sample_units_kernel(SampleArgs a
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const bool in = key[e] > bound;
+        const bool in = v[e] > limit;
         const uint64_t m = __ballot(in);
         if (m) {
           if (in) {
             const int64_t i = at + ((e / P) * kWave + lane) * P + e % P - row.skip;
-            list[n + __popcll(m & below)] = (uint64_t)key[e] << 32 | (uint32_t)~(uint32_t)i;
+            list[n + __popcll(m & below)] = (uint64_t)key_of(v[e]) << 32 | (uint32_t)~(uint32_t)i;
           }
           n += __popcll(m);
         }
@@ -403,20 +461,14 @@ __device__ Cut descend(const Row<T> &row, const Weigh &wg, bool by_mass, bool wi
       sh.hist.mass[i] = 0;
     }
     __syncthreads();
-#pragma unroll 2
-    for (int64_t s = (int64_t)threadIdx.x * P; s < row.end; s += kThreads * P) {
-      float v[P];
-      row.load(s, v);
-#pragma unroll
-      for (int e = 0; e < P; ++e) {
-        const uint32_t k = key_of(v[e]);
-        if (k > kKeyNegInf && (level == 0 || k >> shift == prefix)) {
-          const uint32_t d = (k >> next) & (bins - 1);
-          atomicAdd(&sh.hist.count[d], 1u);
-          if (with_mass) atomicAdd(&sh.hist.mass[d], (unsigned long long)wg.mass(wg.weight(v[e])));
-        }
+    row.template each<4>((int64_t)threadIdx.x * P, kThreads * P, row.end, [&](float v, int64_t) {
+      const uint32_t k = key_of(v);
+      if (k > kKeyNegInf && (level == 0 || k >> shift == prefix)) {
+        const uint32_t d = (k >> next) & (bins - 1);
+        atomicAdd(&sh.hist.count[d], 1u);
+        if (with_mass) atomicAdd(&sh.hist.mass[d], (unsigned long long)wg.mass(wg.weight(v)));
       }
-    }
+    });
     __syncthreads();
     if (threadIdx.x < kWave) {   // wave 0 scans the bins from the top, 64 at a time
       const int lane = threadIdx.x;
@@ -501,14 +553,7 @@ __device__ void draw(const SampleArgs &a, int64_t r, const Row<T> &row, const We
     const int64_t s0 = min(beg + seg * wave, end), s1 = min(s0 + seg, end);
     uint64_t m = 0, t = 0;
     if (wide) {
-#pragma unroll 2
-      for (int64_t s = s0 + lane * P; s < s1; s += kWave * P) {
-        float v[P];
-        row.load(s, v);
-#pragma unroll
-        for (int e = 0; e < P; ++e)
-          if (s + e < s1) take(v[e], m, t);
-      }
+      row.template each<4>(s0 + lane * P, kWave * P, s1, [&](float v, int64_t) { take(v, m, t); });
     } else {
       for (int64_t s = s0 + lane; s < s1; s += kWave) take(row.at(s), m, t);
     }
@@ -748,16 +793,33 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, con
 
   // the listed elements above the bound, sorted
   if (per_row > 0) {
+    // a wave takes units wave, wave + 16, ..; lists are read whole (entries
+    // behind a unit's count are whatever the workspace held) so that count and
+    // entries are one round trip
     __syncthreads();
-    for (int64_t i = threadIdx.x; i < (int64_t)per_row * kCand; i += kThreads) {
-      const int unit = (int)(i / kCand), e = (int)(i % kCand);
-      if (e < (int)units[unit].count) {
-        const uint64_t x = lists[i];
-        if ((uint32_t)(x >> 32) > bound) {
-          const uint32_t at = atomicAdd(&sh.listed, 1u);
-          if (at < kList) sh.list.entry[at] = x;
-        }
+    constexpr int kU = 5;
+    for (int base = wave; base < per_row; base += kU * kWaves) {
+      uint64_t x[kU][2];
+      uint32_t n[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int unit = min(base + u * kWaves, per_row - 1);
+        n[u] = base + u * kWaves < per_row ? units[unit].count : 0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) x[u][e] = lists[(int64_t)unit * kCand + e * kWave + lane];
       }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bool in = e * kWave + lane < (int)n[u] && (uint32_t)(x[u][e] >> 32) > bound;
+          const uint64_t m = __ballot(in);
+          if (!m) continue;
+          uint32_t at = 0;
+          if (lane == 0) at = atomicAdd(&sh.listed, (uint32_t)__popcll(m));
+          at = __shfl(at, 0, kWave) + __popcll(m & ((1ull << lane) - 1));
+          if (in && at < kList) sh.list.entry[at] = x[u][e];
+        }
     }
   }
   __syncthreads();
