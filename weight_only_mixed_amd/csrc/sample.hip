@@ -41,9 +41,8 @@ constexpr int kList = 2048;              // sorted entries of a row
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;   // key_of(-inf): the smallest key
 
 struct Unit {
-  uint64_t best;     // (key, ~index): the largest element, its lowest index
-  double mass;       // sum of exp((l - ref) / T), where the row needs it
-  float ref;
+  double mass;       // sum of exp((l - top) / T), where the row needs it
+  float top;         // the largest element
   uint32_t bound;    // every element with a key above it is listed
   uint32_t count;
   uint32_t pad;
@@ -247,11 +246,12 @@ struct Cuts {
   }
 };
 
-// The n-th largest of the wave's keys, n <= their number.
+// The n-th largest of the wave's keys, n <= their number, cut to its bits above
+// `low`: at least n keys are not below it.
 template <int PER>
-__device__ uint32_t wave_nth(const uint32_t (&key)[PER], int n) {
+__device__ uint32_t wave_nth(const uint32_t (&key)[PER], int n, int low) {
   uint32_t t = 0;
-  for (int b = 31; b >= 0; --b) {
+  for (int b = 31; b >= low; --b) {
     const uint32_t c = t | 1u << b;
     int have = 0;
 #pragma unroll
@@ -261,10 +261,12 @@ __device__ uint32_t wave_nth(const uint32_t (&key)[PER], int n) {
   return t;
 }
 
+// Values are compared as they are loaded: a NaN exceeds no bound and is never
+// listed, an infinity is tamed where it is used.
 template <int T>
-__global__ __launch_bounds__(kUnitThreads) void sample_units_kernel(SampleArgs a, Unit *units,
-                                                                    uint64_t *lists, int per_row,
-                                                                    int steps, int keep) {
+__global__ __launch_bounds__(kUnitThreads, 4) void sample_units_kernel(SampleArgs a, Unit *units,
+                                                                       uint64_t *lists, int per_row,
+                                                                       int steps, int keep) {
   __shared__ uint64_t lds[kUnitThreads / kWave][kCand];
   constexpr int P = Logit<T>::kPer, V = 16 / P;
   const int lane = threadIdx.x & (kWave - 1);
@@ -280,14 +282,14 @@ __global__ __launch_bounds__(kUnitThreads) void sample_units_kernel(SampleArgs a
     const Cuts cuts(a, r);
     const bool with_mass = cuts.row_mass(a.vocab);
     const double inv_t = 1.0 / (double)cuts.temp;
-    const int64_t beg = (int64_t)unit * steps * kBatch;
+    const int beg = unit * steps * kBatch;   // slots fit an int: vocab <= 2^24
     uint32_t bound = kKeyNegInf;
+    float limit = -INFINITY;                 // v > limit: key above the bound
     int n = 0;
-    uint64_t best = 0;
     double mass = 0.0;
-    float ref = -INFINITY;
+    float top = -INFINITY, lane_top = -INFINITY;
     typename Logit<T>::Vec next[V];
-    auto fetch = [&](int64_t at) {
+    auto fetch = [&](int at) {
       if (row.inside(at, at + kBatch)) {
 #pragma unroll
         for (int j = 0; j < V; ++j) next[j] = row.raw(at + (j * kWave + lane) * P);
@@ -298,43 +300,40 @@ __global__ __launch_bounds__(kUnitThreads) void sample_units_kernel(SampleArgs a
     };
     fetch(beg);
     for (int s = 0; s < steps; ++s) {
-      const int64_t at = beg + (int64_t)s * kBatch;
+      const int at = beg + s * kBatch;
       if (at >= row.end) break;
       float v[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = tame(Logit<T>::get(next[e / P], e % P));
+      for (int e = 0; e < 16; ++e) v[e] = Logit<T>::get(next[e / P], e % P);
       if (s + 1 < steps) fetch(at + kBatch);
       float mx = v[0];
 #pragma unroll
       for (int e = 1; e < 16; ++e) mx = fmaxf(mx, v[e]);
-      const uint32_t kmax = key_of(mx);
+      mx = tame(mx);
+      lane_top = fmaxf(lane_top, mx);
       if (s == 0) {
         // `keep` distinct elements are at least the keep-th largest lane maximum
-        const uint32_t one[1] = {kmax};
-        if (__popcll(__ballot(kmax > kKeyNegInf)) >= keep) bound = wave_nth(one, keep) - 1;
+        const uint32_t one[1] = {key_of(mx)};
+        if (__popcll(__ballot(mx > -INFINITY)) >= keep) {
+          bound = max(wave_nth(one, keep, 14), kKeyNegInf + 1) - 1;
+          limit = limit_of(bound);
+        }
       }
       if (with_mass) {
-        const float top = wave_max(mx);
-        if (top > ref) {
-          if (ref != -INFINITY) mass *= exp_neg(((double)ref - (double)top) * inv_t);
-          ref = top;
+        const float t = wave_max(mx);
+        if (t > top) {
+          if (top != -INFINITY) mass *= exp_neg(((double)top - (double)t) * inv_t);
+          top = t;
         }
-        if (ref != -INFINITY) {
+        if (top != -INFINITY) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            mass += v[e] == -INFINITY ? 0.0 : exp_neg(((double)v[e] - (double)ref) * inv_t);
-        }
-      }
-      if ((uint32_t)(best >> 32) < kmax) {   // per lane: its own lowest index of a new largest
-#pragma unroll
-        for (int e = 15; e >= 0; --e)
-          if (v[e] == mx) {
-            const int64_t i = at + ((e / P) * kWave + lane) * P + e % P - row.skip;
-            best = (uint64_t)kmax << 32 | (uint32_t)~(uint32_t)i;
+          for (int e = 0; e < 16; ++e) {
+            const float x = tame(v[e]);
+            mass += x == -INFINITY ? 0.0 : exp_neg(((double)x - (double)top) * inv_t);
           }
+        }
       }
-      if (!__any(kmax > bound)) continue;
-      float limit = limit_of(bound);   // v > limit: key above the bound
+      if (!__any(mx > limit)) continue;
       int more = 0;
 #pragma unroll
       for (int e = 0; e < 16; ++e) more += __popcll(__ballot(v[e] > limit));
@@ -342,14 +341,14 @@ __global__ __launch_bounds__(kUnitThreads) void sample_units_kernel(SampleArgs a
         // too many: the bound moves to the keep-th largest of list and batch
         uint32_t all[18];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) all[e] = key_of(v[e]);
+        for (int e = 0; e < 16; ++e) all[e] = key_of(tame(v[e]));
         uint64_t old[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           old[e] = e * kWave + lane < n ? list[e * kWave + lane] : 0;
           all[16 + e] = (uint32_t)(old[e] >> 32);
         }
-        bound = wave_nth(all, keep);
+        bound = wave_nth(all, keep, 0);
         limit = limit_of(bound);
         n = 0;
 #pragma unroll
@@ -362,22 +361,22 @@ __global__ __launch_bounds__(kUnitThreads) void sample_units_kernel(SampleArgs a
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const bool in = v[e] > limit;
+        const bool in = tame(v[e]) > limit;
         const uint64_t m = __ballot(in);
         if (m) {
           if (in) {
-            const int64_t i = at + ((e / P) * kWave + lane) * P + e % P - row.skip;
-            list[n + __popcll(m & below)] = (uint64_t)key_of(v[e]) << 32 | (uint32_t)~(uint32_t)i;
+            const int i = at + ((e / P) * kWave + lane) * P + e % P - row.skip;
+            list[n + __popcll(m & below)] = (uint64_t)key_of(tame(v[e])) << 32 | (uint32_t)~(uint32_t)i;
           }
           n += __popcll(m);
         }
       }
     }
-    best = wave_max_u64(best);
+    top = wave_max(lane_top);
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) mass += __shfl_xor(mass, o, kWave);
     const int64_t slot = r * per_row + unit;
-    if (lane == 0) units[slot] = Unit{best, mass, ref, bound, (uint32_t)n, 0u};
+    if (lane == 0) units[slot] = Unit{mass, top, bound, (uint32_t)n, 0u};
     for (int e = lane; e < n; e += kWave) lists[slot * kCand + e] = list[e];
   }
 }
@@ -389,17 +388,41 @@ struct Shared {
       unsigned long long mass[kBins];
     } hist;
     struct {
-      uint64_t entry[kList];          // sorted: (key, ~index) descending
+      uint64_t entry[kList];          // (key, ~index)
       unsigned long long mass[kList];
-      uint64_t order[kList];
+      union {
+        uint64_t order[kList];
+        uint32_t count[kBins];
+      };
     } list;
   };
   uint64_t a[kWaves], b[kWaves];
   double d[kWaves];
-  uint32_t digit, listed;
+  uint32_t digit, listed, some;
   uint64_t above_n, above_m;
   int64_t pos;
 };
+
+// Inclusive sum over the threads before and at this one; `total` over all.
+__device__ __forceinline__ uint64_t block_scan_u64(uint64_t v, uint64_t &total, Shared &sh) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const uint64_t up = __shfl_up((unsigned long long)v, o, kWave);
+    if (lane >= o) v += up;
+  }
+  __syncthreads();
+  if (lane == kWave - 1) sh.a[wave] = v;
+  __syncthreads();
+  total = 0;
+  uint64_t before = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (w == wave) before = total;
+    total += sh.a[w];
+  }
+  return v + before;
+}
 
 __device__ __forceinline__ uint64_t block_max_u64(uint64_t v, Shared &sh) {
   v = wave_max_u64(v);
@@ -521,6 +544,124 @@ __device__ Cut descend(const Row<T> &row, const Weigh &wg, bool by_mass, bool wi
   return Cut{prefix, above_n, above_m, ties};
 }
 
+// The kept prefix that a count or a mass asks for: keys above tau and the first
+// `quota` elements equal to it, weighing `mass`.
+struct Prefix {
+  uint32_t tau;
+  uint64_t quota, mass;
+};
+
+// The shortest prefix of the row's order with want_n elements (by_mass false)
+// or of mass want_m.  One histogram over 2048 bins of (max - l) / T, 1/64 wide
+// (the map is monotone in l, so bins are runs of the order), then only the
+// bin where the cut falls is gathered and sorted.  A bin of more than kList
+// elements (ties, or the far tail in the last bin) takes the radix descent.
+template <int T>
+__device__ Prefix row_prefix(const Row<T> &row, const Weigh &wg, bool by_mass, bool with_mass,
+                             uint64_t want_n, double want_m, Shared &sh) {
+  constexpr int P = Logit<T>::kPer;
+  const float top = (float)wg.max, step = (float)fmin(64.0 * wg.inv_t, 1e30);
+  auto bin_of = [&](float v) { return (int)fminf((top - v) * step, (float)(kBins - 1)); };
+  __syncthreads();
+  for (int i = threadIdx.x; i < kBins; i += kThreads) {
+    sh.hist.count[i] = 0;
+    sh.hist.mass[i] = 0;
+  }
+  if (threadIdx.x == 0) {
+    sh.listed = 0;
+    sh.digit = kBins;
+  }
+  __syncthreads();
+  row.template each<4>((int64_t)threadIdx.x * P, kThreads * P, row.end, [&](float v, int64_t) {
+    if (v == -INFINITY) return;
+    const int d = bin_of(v);
+    if (!by_mass) atomicAdd(&sh.hist.count[d], 1u);
+    if (with_mass) atomicAdd(&sh.hist.mass[d], (unsigned long long)wg.mass(wg.weight(v)));
+  });
+  __syncthreads();
+  const int b0 = 2 * threadIdx.x;
+  uint64_t n[2] = {sh.hist.count[b0], sh.hist.count[b0 + 1]};
+  uint64_t m[2] = {sh.hist.mass[b0], sh.hist.mass[b0 + 1]};
+  uint64_t total;
+  const uint64_t run_n = block_scan_u64(n[0] + n[1], total, sh);
+  const uint64_t run_m = with_mass ? block_scan_u64(m[0] + m[1], total, sh) : 0;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const uint64_t through_n = e ? run_n : run_n - n[1], through_m = e ? run_m : run_m - m[1];
+    const bool hit = by_mass ? (double)through_m >= want_m && !((double)(through_m - m[e]) >= want_m)
+                             : through_n >= want_n && through_n - n[e] < want_n;
+    if (hit) {   // one bin, or none where rounding put the mass behind the last
+      sh.digit = (uint32_t)(b0 + e);
+      sh.above_n = through_n - n[e];
+      sh.above_m = through_m - m[e];
+    }
+  }
+  __syncthreads();
+  const int bin = (int)sh.digit;
+  const uint64_t above_n = sh.above_n, above_m = sh.above_m;
+  if (bin < kBins - 1) {
+    row.template each<4>((int64_t)threadIdx.x * P, kThreads * P, row.end, [&](float v, int64_t slot) {
+      if (v == -INFINITY || bin_of(v) != bin) return;
+      const uint32_t at = atomicAdd(&sh.listed, 1u);
+      if (at < kList)
+        sh.list.entry[at] = (uint64_t)key_of(v) << 32 | (uint32_t)~(uint32_t)(slot - row.skip);
+    });
+    __syncthreads();
+    const int listed = (int)sh.listed;
+    if (listed <= kList) {
+      int size = kWave;
+      while (size < listed) size <<= 1;
+      for (int i = listed + threadIdx.x; i < size; i += kThreads) sh.list.entry[i] = 0;
+      block_sort(sh.list.entry, size);
+      uint64_t w[2] = {0, 0};
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (with_mass && b0 + e < listed)
+          w[e] = wg.mass(wg.weight(value_of((uint32_t)(sh.list.entry[b0 + e] >> 32))));
+      const uint64_t run = with_mass ? block_scan_u64(w[0] + w[1], total, sh) + above_m : above_m;
+      if (threadIdx.x == 0) sh.pos = -1;
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint64_t through = e ? run : run - w[1];
+        const bool hit = b0 + e < listed &&
+                         (by_mass ? (double)through >= want_m && !((double)(through - w[e]) >= want_m)
+                                  : (uint64_t)(b0 + e) == want_n - above_n - 1);
+        if (hit) {
+          sh.pos = b0 + e;
+          sh.above_m = through;
+        }
+      }
+      __syncthreads();
+      const int at = (int)sh.pos;
+      if (at >= 0) {
+        const uint32_t tau = (uint32_t)(sh.list.entry[at] >> 32);
+        // entries equal to tau up to the cut
+        uint64_t q = 0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          q += b0 + e <= at && (uint32_t)(sh.list.entry[b0 + e] >> 32) == tau;
+        block_scan_u64(q, total, sh);
+        const Prefix out{tau, total, sh.above_m};
+        __syncthreads();
+        return out;
+      }
+    }
+  }
+  const Cut c = descend<T>(row, wg, by_mass, with_mass, want_n, want_m, sh);
+  const uint64_t w = with_mass ? wg.mass(wg.weight(value_of(c.tau))) : 0;
+  uint64_t q;
+  if (by_mass) {
+    const double need = want_m - (double)c.above_m;
+    q = w > 0 ? need > 0.0 ? (uint64_t)ceil(need / (double)w) : 1 : c.ties;
+    if (q < 1) q = 1;
+  } else {
+    q = want_n > c.above_n ? want_n - c.above_n : 0;
+  }
+  if (q > c.ties) q = c.ties;
+  return Prefix{c.tau, q, c.above_m + q * w};
+}
+
 // Draws from the elements with key > tau and the first `quota` ones equal to
 // it, of weight >= min_w, among slots [beg, end): a descent over index
 // segments, one per wave, to the 64 slots that hold the answer.  `target` < 0:
@@ -632,7 +773,7 @@ __device__ void draw_listed(const SampleArgs &a, int64_t r, const Weigh &wg, int
   while (size < n) size <<= 1;
   for (int i = threadIdx.x; i < size; i += kThreads)   // ~index descending: index ascending
     sh.list.order[i] = i < n ? (sh.list.entry[i] & 0xFFFFFFFFull) << 32 | (uint32_t)i : 0;
-  block_sort(sh.list.order, size);
+  block_sort(sh.list.order, size);   // starts with a barrier
   // each thread two neighbours, a scan over threads
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int i0 = 2 * threadIdx.x;
@@ -674,6 +815,76 @@ __device__ void draw_listed(const SampleArgs &a, int64_t r, const Weigh &wg, int
   }
 }
 
+// At most this many listed elements are ranked by comparing all pairs.
+constexpr int kPairs = 256;
+
+// Cuts and draws among n <= kPairs listed elements, in any order: kThreads / n
+// threads share an element and compare it with all others.  n_k: elements that
+// top_k leaves; want < 0: no top_p; `of_list`: want is p of the mass of the
+// first n_k, not a mass.
+__device__ void cut_pairs(const SampleArgs &a, int64_t r, const Weigh &wg, int n, int64_t n_k,
+                          double want, bool of_list, double min_w, Shared &sh) {
+  int size = 16;
+  while (size < n) size <<= 1;
+  const int per = kThreads / size;               // 4 .. 64 neighbouring lanes
+  const int i = threadIdx.x / per, part = threadIdx.x % per;
+  const bool real = i < n;
+  const uint64_t x = real ? sh.list.entry[i] : 0;
+  double w = 0.0;
+  uint64_t m = 0;
+  if (real) {
+    w = wg.weight(value_of((uint32_t)(x >> 32)));
+    m = wg.mass(w);
+    if (part == 0) sh.list.mass[i] = m;
+  }
+  __syncthreads();
+  uint32_t rank = 0;
+  uint64_t run = 0;                              // mass of the elements before it and its own
+  for (int j = part; j < n; j += per) {
+    const uint64_t y = sh.list.entry[j];
+    if (y >= x) {
+      rank += y > x;
+      run += sh.list.mass[j];
+    }
+  }
+  for (int o = 1; o < per; o <<= 1) {
+    rank += __shfl_xor(rank, o, kWave);
+    run += __shfl_xor((unsigned long long)run, o, kWave);
+  }
+  if (real && part == 0 && rank == n_k - 1) sh.above_m = run;
+  __syncthreads();
+  if (of_list) want = fmax(want * (double)sh.above_m, 1.0);
+  const bool keep = real && rank < n_k && w >= min_w &&
+                    (want < 0.0 || rank == 0 || (double)(run - m) < want);
+  if (real && part == 0 && !keep) sh.list.mass[i] = 0;
+  __syncthreads();
+  uint64_t cum = 0, total = 0;                   // by index: ~index not below its own
+  for (int j = part; j < n; j += per) {
+    const uint64_t mj = sh.list.mass[j];
+    total += mj;
+    if ((uint32_t)sh.list.entry[j] >= (uint32_t)x) cum += mj;
+  }
+  for (int o = 1; o < per; o <<= 1) {
+    cum += __shfl_xor((unsigned long long)cum, o, kWave);
+    total += __shfl_xor((unsigned long long)total, o, kWave);
+  }
+  const float u = a.u[r];
+  const double target = fmin((double)(u > 0.f ? u : 0.f) * (double)total, (double)(total - 1));
+  // the element whose share holds the target, or (rounding) the last of any mass
+  const bool holds = keep && m > 0 && part == 0;
+  if (holds && cum == total) sh.pos = i;
+  __syncthreads();
+  if (holds && (double)cum > target && !((double)(cum - m) > target)) sh.pos = i;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const uint64_t e = sh.list.entry[sh.pos];
+    a.tokens[r] = (int32_t)~(uint32_t)e;
+    if (a.logprobs)
+      a.logprobs[r] = (float)(((double)value_of((uint32_t)(e >> 32)) - wg.max) * wg.inv_t -
+                              log((double)total / wg.unit));
+  }
+}
+
 // per_row = 0: the row is listed whole, no units.
 template <int T>
 __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, const Unit *units,
@@ -685,15 +896,19 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, con
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const Row<T> row(a, r);
   const Cuts cuts(a, r);
+  const int unit_slots = steps * kBatch;
   units += r * per_row;
   lists += r * per_row * kCand;
 
   // the largest logit and the bound above which every element is listed
-  uint64_t best = 0;
   uint32_t bound = kKeyNegInf;
-  if (threadIdx.x == 0) sh.listed = 0;
+  uint64_t best = 0;                   // (key, bound) or (key, ~index)
+  if (threadIdx.x == 0) {
+    sh.listed = 0;
+    sh.some = 0;
+  }
+  __syncthreads();
   if (per_row == 0) {
-    __syncthreads();
     for (int64_t s = (int64_t)threadIdx.x * P; s < row.end; s += kThreads * P) {
       float v[P];
       row.load(s, v);
@@ -708,15 +923,28 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, con
     }
     best = block_max_u64(best, sh);
   } else {
+    uint32_t key = 0;
     for (int i = threadIdx.x; i < per_row; i += kThreads) {
-      best = units[i].best > best ? units[i].best : best;
+      key = max(key, key_of(units[i].top));
       bound = max(bound, units[i].bound);
     }
-    best = block_max_u64(best, sh);
+    best = block_max_u64((uint64_t)key << 32, sh);
     bound = (uint32_t)block_max_u64(bound, sh);
   }
   const float top = value_of((uint32_t)(best >> 32));
   if (top == -INFINITY || cuts.greedy()) {
+    if (per_row > 0 && top != -INFINITY) {
+      // its lowest index: in the first unit that reaches it
+      uint64_t first = 0;
+      for (int i = threadIdx.x; i < per_row; i += kThreads)
+        if (units[i].top == top) first = max(first, (uint64_t)(uint32_t)~(uint32_t)i);
+      const int unit = (int)~(uint32_t)block_max_u64(first, sh);
+      const int64_t s0 = (int64_t)unit * unit_slots, s1 = min(s0 + unit_slots, row.end);
+      best = 0;
+      for (int64_t s = s0 + threadIdx.x; s < s1; s += kThreads)
+        if (row.at(s) == top) best = max(best, (uint64_t)(uint32_t)~(uint32_t)(s - row.skip));
+      best = block_max_u64(best, sh);
+    }
     if (threadIdx.x == 0) {
       a.tokens[r] = top == -INFINITY ? -1 : (int32_t)~(uint32_t)best;
       if (a.logprobs) a.logprobs[r] = top == -INFINITY ? -INFINITY : 0.f;
@@ -733,7 +961,7 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, con
     // thread w * 64 + l takes units l + 64 w + 1024 n ...: a fixed order
     double m = 0.0;
     for (int i = threadIdx.x; i < per_row; i += kThreads)
-      if (units[i].ref != -INFINITY) m += units[i].mass * wg.weight(units[i].ref);
+      if (units[i].top != -INFINITY) m += units[i].mass * wg.weight(units[i].top);
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) m += __shfl_xor(m, o, kWave);
     __syncthreads();
@@ -747,14 +975,15 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, con
     // the unit that holds the draw: wave 0 scans the units' masses by index
     const float u = a.u[r];
     const double target = fmin((double)(u > 0.f ? u : 0.f), 1.0 - 0x1p-53) * row_mass;
+    __syncthreads();
     if (wave == 0) {
       double before = 0.0;
       int64_t pick = -1, last = 0;
       double pick_before = 0.0, last_before = 0.0;
       for (int base = 0; base < per_row && pick < 0; base += kWave) {
         const int i = base + lane;
-        const double m = i < per_row && units[i].ref != -INFINITY
-                             ? units[i].mass * wg.weight(units[i].ref) * wg.unit : 0.0;
+        const double m = i < per_row && units[i].top != -INFINITY
+                             ? units[i].mass * wg.weight(units[i].top) * wg.unit : 0.0;
         double c = m;
 #pragma unroll
         for (int o = 1; o < kWave; o <<= 1) {
@@ -762,7 +991,7 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, con
           if (lane >= o) c += up;
         }
         // (a unit of less mass than elements may hold no element of any)
-        const bool holds = m >= (double)steps * kBatch;
+        const bool holds = m >= (double)unit_slots;
         const uint64_t some = __ballot(holds);
         const uint64_t hit = __ballot(holds && before + c > target);
         if (hit) {
@@ -784,19 +1013,17 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, con
     __syncthreads();
     const int64_t at = sh.pos;
     const double rest = target - sh.d[0];
-    const int64_t unit = (int64_t)steps * kBatch;
     __syncthreads();
-    draw<T>(a, r, row, wg, 0u, 0, 0.0, at * unit, min((at + 1) * unit, row.end),
+    draw<T>(a, r, row, wg, 0u, 0, 0.0, at * unit_slots, min((at + 1) * unit_slots, row.end),
             rest > 0.0 ? rest : 0.0, row_mass, sh);
     return;
   }
 
-  // the listed elements above the bound, sorted
+  // the listed elements above the bound
   if (per_row > 0) {
     // a wave takes units wave, wave + 16, ..; lists are read whole (entries
     // behind a unit's count are whatever the workspace held) so that count and
     // entries are one round trip
-    __syncthreads();
     constexpr int kU = 5;
     for (int base = wave; base < per_row; base += kU * kWaves) {
       uint64_t x[kU][2];
@@ -823,15 +1050,86 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, con
     }
   }
   __syncthreads();
-  const int listed = (int)sh.listed;
+  int listed = (int)sh.listed;
   const bool whole = bound == kKeyNegInf && listed <= kList;   // every element above -inf
-  if (listed <= kList && listed > 0) {
+  const bool k_inside = listed <= kList && (cuts.k <= listed || whole);
+  const int64_t n_k = min<int64_t>(cuts.k, listed);
+  const int i0 = 2 * threadIdx.x;
+  // whether the kept set is known to end inside the list
+  bool inside = listed > 0 && listed <= kList;
+  if (inside && (listed > kPairs || !k_inside)) {
+    // Narrow the list to a shorter prefix that still holds the kept set, by a
+    // histogram of its keys: through the n_k-th element, or the nucleus; and
+    // where no mass of the first k is asked for, to the elements that min_p
+    // leaves.
+    const uint32_t top_key = (uint32_t)(best >> 32), span = top_key - bound - 1;
+    const int shift = max(0, 32 - 11 - (span ? __builtin_clz(span) : 32));
+    uint64_t x[2], m[2];
+    bool heavy[2];
+    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.list.count[i] = 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      x[e] = i0 + e < listed ? sh.list.entry[i0 + e] : 0;
+      const double w = i0 + e < listed && !k_inside ? wg.weight(value_of((uint32_t)(x[e] >> 32))) : 0.0;
+      heavy[e] = w >= cuts.min_w;
+      m[e] = wg.mass(w);
+      sh.list.mass[i0 + e] = 0;   // the histogram's masses (kBins == kList)
+      if (i0 + e < listed && !k_inside && !heavy[e]) sh.some = 1;   // min_p ends inside
+    }
+    auto bin_of = [&](uint64_t v) { return (int)((top_key - (uint32_t)(v >> 32)) >> shift); };
+    __syncthreads();
+    const bool by_mass = !k_inside && cuts.p < 1.0;
+    if (k_inside || by_mass) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (i0 + e < listed) {
+          if (by_mass) atomicAdd(&sh.list.mass[bin_of(x[e])], (unsigned long long)m[e]);
+          else atomicAdd(&sh.list.count[bin_of(x[e])], 1u);
+        }
+    }
+    if (threadIdx.x == 0) {
+      sh.digit = kBins;
+      sh.listed = 0;
+    }
+    __syncthreads();
+    if (k_inside || by_mass) {
+      const uint64_t h0 = by_mass ? sh.list.mass[i0] : sh.list.count[i0];
+      const uint64_t h1 = by_mass ? sh.list.mass[i0 + 1] : sh.list.count[i0 + 1];
+      uint64_t all;
+      const uint64_t run1 = block_scan_u64(h0 + h1, all, sh), run0 = run1 - h1;
+      const double want = by_mass ? fmax(cuts.p * row_mass, 1.0) : (double)n_k;
+      if ((double)run0 >= want && !((double)(run0 - h0) >= want)) sh.digit = (uint32_t)i0;
+      else if ((double)run1 >= want && !((double)(run1 - h1) >= want)) sh.digit = (uint32_t)i0 + 1;
+      __syncthreads();
+    }
+    const int through = (int)sh.digit;    // the last bin that the prefix needs
+    const bool min_ends = sh.some != 0;
+    if (!k_inside)
+      inside = cuts.k == a.vocab ? (by_mass && through < kBins) || min_ends
+                                 : !(cuts.p < 1.0) && min_ends;
+    __syncthreads();
+    if (inside) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (i0 + e < listed && (k_inside || heavy[e]) && bin_of(x[e]) <= through)
+          sh.list.entry[atomicAdd(&sh.listed, 1u)] = x[e];
+      __syncthreads();
+      listed = (int)sh.listed;
+    }
+  }
+  if (inside) {
+    const bool nucleus = cuts.p < 1.0;
+    const double want = !nucleus ? -1.0 : k_inside ? cuts.p : fmax(cuts.p * row_mass, 1.0);
+    const int64_t first = min<int64_t>(n_k, listed);
+    if (listed <= kPairs) {
+      cut_pairs(a, r, wg, listed, first, want, nucleus && k_inside, cuts.min_w, sh);
+      return;
+    }
     int size = kWave;
     while (size < listed) size <<= 1;
     for (int i = listed + threadIdx.x; i < size; i += kThreads) sh.list.entry[i] = 0;
     block_sort(sh.list.entry, size);
     // masses, their running sum, and where each cut falls
-    const int i0 = 2 * threadIdx.x;
     uint64_t m[2];
     int heavy = 0;   // entries of weight >= min_w
 #pragma unroll
@@ -844,57 +1142,26 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, con
         heavy += w >= cuts.min_w;
       }
     }
-    uint64_t c = m[0] + m[1];
-#pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-      const uint64_t up = __shfl_up((unsigned long long)c, o, kWave);
-      if (lane >= o) c += up;
-    }
-    const uint64_t hw = wave_sum_u64((uint64_t)heavy);
-    __syncthreads();
-    if (lane == kWave - 1) {
-      sh.a[wave] = c;
-      sh.b[wave] = hw;
-    }
-    __syncthreads();
-    uint64_t before = 0, all = 0, n_min = 0;
-    for (int w = 0; w < kWaves; ++w) {
-      if (w == wave) before = all;
-      all += sh.a[w];
-      n_min += sh.b[w];
-    }
-    const uint64_t run1 = before + c, run0 = run1 - m[1];   // running mass through i0, i0 + 1
-    const int64_t n_k = min<int64_t>(cuts.k, listed);
-    const bool k_inside = cuts.k <= listed || whole;
-    // mass that top_p refers to
-    if (i0 == n_k - 1) sh.above_m = run0;
-    if (i0 + 1 == n_k - 1) sh.above_m = run1;
+    uint64_t all, n_min;
+    block_scan_u64((uint64_t)heavy, n_min, sh);
+    const uint64_t run1 = block_scan_u64(m[0] + m[1], all, sh), run0 = run1 - m[1];
+    if (i0 == first - 1) sh.above_m = run0;      // mass of the first k
+    if (i0 + 1 == first - 1) sh.above_m = run1;
     if (threadIdx.x == 0) sh.pos = listed;
     __syncthreads();
-    bool inside = k_inside;
-    int64_t n = n_k;
-    if (cuts.p < 1.0) {
-      const double of = k_inside ? (double)sh.above_m : row_mass;
-      const double want = fmax(cuts.p * of, 1.0);
+    int64_t n = min<int64_t>(first, (int64_t)n_min);
+    if (nucleus) {
+      const double mass = k_inside ? fmax(want * (double)sh.above_m, 1.0) : want;
       // the first entry whose running mass reaches the wanted one
-      if (i0 < listed && (double)run0 >= want && !((double)(run0 - m[0]) >= want)) sh.pos = i0;
-      else if (i0 + 1 < listed && (double)run1 >= want && !((double)(run1 - m[1]) >= want))
+      if (i0 < listed && (double)run0 >= mass && !((double)(run0 - m[0]) >= mass)) sh.pos = i0;
+      else if (i0 + 1 < listed && (double)run1 >= mass && !((double)(run1 - m[1]) >= mass))
         sh.pos = i0 + 1;
       __syncthreads();
-      const int64_t n_p = sh.pos < listed ? sh.pos + 1 : listed;
-      // without a top-k inside the list the nucleus, or min_p, has to end inside it
-      if (!k_inside)
-        inside = cuts.k == a.vocab && (sh.pos < listed || (int64_t)n_min < listed);
-      n = min(n, n_p);
-    } else if (!k_inside) {
-      inside = (int64_t)n_min < listed;   // min_p alone cuts the list
-    }
-    if (cuts.min_w > 0.0) n = min<int64_t>(n, (int64_t)n_min);
-    if (inside) {
+      n = min<int64_t>(n, sh.pos + 1);
       __syncthreads();
-      draw_listed(a, r, wg, (int)n, sh);
-      return;
     }
+    draw_listed(a, r, wg, (int)n, sh);
+    return;
   }
 
   // the kept set ends outside the list
@@ -902,27 +1169,19 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, con
   uint64_t quota = 0;
   double of_mass = row_mass;
   if (cuts.k < a.vocab) {
-    const bool with_mass = cuts.p < 1.0;
-    const Cut c = descend<T>(row, wg, false, with_mass, (uint64_t)cuts.k, 0.0, sh);
+    const Prefix c = row_prefix<T>(row, wg, false, cuts.p < 1.0, (uint64_t)cuts.k, 0.0, sh);
     tau = c.tau;
-    quota = (uint64_t)cuts.k > c.above_n ? (uint64_t)cuts.k - c.above_n : 0;
-    const uint64_t ties = quota < c.ties ? quota : c.ties;
-    of_mass = (double)(c.above_m + ties * wg.mass(wg.weight(value_of(tau))));
+    quota = c.quota;
+    of_mass = (double)c.mass;
   }
   if (cuts.p < 1.0) {
     // shortest prefix with mass >= p * of_mass; at least one token
-    const double want = fmax(cuts.p * of_mass, 1.0);
-    const Cut c = descend<T>(row, wg, true, true, 0, want, sh);
-    const uint64_t w = wg.mass(wg.weight(value_of(c.tau)));
-    const double need = want - (double)c.above_m;
-    uint64_t q = w > 0 && need > 0.0 ? (uint64_t)ceil(need / (double)w) : w > 0 ? 1 : c.ties;
-    if (q < 1) q = 1;
-    if (q > c.ties) q = c.ties;
+    const Prefix c = row_prefix<T>(row, wg, true, true, 0, fmax(cuts.p * of_mass, 1.0), sh);
     if (c.tau > tau) {
       tau = c.tau;
-      quota = q;
-    } else if (c.tau == tau && q < quota) {
-      quota = q;
+      quota = c.quota;
+    } else if (c.tau == tau && c.quota < quota) {
+      quota = c.quota;
     }
   }
   __syncthreads();
