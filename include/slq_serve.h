@@ -65,7 +65,7 @@ typedef struct {
  * A token at a negative position, at or behind max_pages * page_size, or on
  * a page number outside 0..pages-1 does not exist: it is not written, reads
  * as 0, and is masked in attention.  cu is clamped to 0..rows.
- * Alignment: 4 bytes.  1 <= max_pages, max_pages * page_size <= 2^30, batch <= 65536,
+ * Alignment: 4 bytes.  1 <= max_pages, max_pages * page_size <= 2^30, batch <= 65535,
  * rows * heads (of the cache or of q) < 2^30.
  */
 typedef struct {

@@ -406,11 +406,327 @@ __global__ __launch_bounds__(kThreads) void kv_attn_kernel(KvAttnArgs a) {
   }
 }
 
+// ---- prompt chunks: many query rows per kv head ----
+//
+// One workgroup of 8 waves takes 256 query rows of a kv head, 32 per wave, and
+// walks the tokens in tiles of 8192 / dim.  A tile's codes are converted once
+// for all waves: every thread loads 16 bytes of K and a 4 x 4 block of V a tile
+// ahead, and writes binary16 to one of two buffers in shared memory, K as
+// [token][dim], V transposed as [dim][token] with the tokens of each 16 in the
+// order of the second product's k slots.  The products are 32x32x16 MFMAs in
+// the transposed form of the decode kernel (S^T = K q^T, O^T = V^T P^T), so
+// probabilities stay in their lane here too and a wave's outputs need no
+// other wave.  Rows in shared memory are swizzled in 16-byte chunks so that
+// both the operand reads (neighbouring rows) and the transposed writes (every
+// fourth row) spread over the banks.
+constexpr int kPromptThreads = 512;
+constexpr int kPromptRows = 256;
+
+typedef float f32x16v __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ f32x16v mfma32h(u32x4_t a, u32x4_t b, f32x16v c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a),
+                                                __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+}
+
+template <int D>
+struct PromptTile {
+  static constexpr int kTok = 8192 / D;          // tokens per tile: 128, 64, 32
+  static constexpr int kGroups = kTok / 16;      // 16-token groups (one page each)
+  static constexpr int kBytes = kTok * D * 2;    // of K, and of V
+  // 16-byte chunk c of K row `tok`
+  static __device__ __forceinline__ int k_at(int tok, int c) {
+    return tok * (D * 2) + ((c ^ (tok & 7)) << 4);
+  }
+  // 16-byte chunk c of V^T row d
+  static __device__ __forceinline__ int v_at(int d, int c) {
+    const int f = D == 256 ? ((d >> 1) ^ (d >> 3)) & 3 : ((d >> 2) ^ (d << 1)) & 7;
+    return d * (kTok * 2) + ((c ^ f) << 4);
+  }
+};
+
+template <int D, bool E4M3>
+__global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs a) {
+  typedef PromptTile<D> Tile;
+  constexpr int TOK = Tile::kTok, GR = Tile::kGroups;
+  constexpr int TT = TOK / 32;      // 32-token tiles of S
+  constexpr int KS = D / 16;        // k steps of q . k
+  constexpr int DT = D / 32;        // 32-dim tiles of the output
+  __shared__ __attribute__((aligned(16))) unsigned char k_lds[2][Tile::kBytes];
+  __shared__ __attribute__((aligned(16))) unsigned char v_lds[2][Tile::kBytes];
+  __shared__ float sk_lds[2][GR], sv_lds[2][GR];   // scales per group; sk < 0: no such tokens
+
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int col = lane & 31, half = lane >> 5;
+  // heads vary fastest over the workgroups: neighbours go to different chiplets,
+  // and the tiles of one head's tokens share a chiplet's L2
+  const int h = blockIdx.x, b = blockIdx.y / a.splits, split = blockIdx.y % a.splits;
+  const KvSpan sp = kv_span(a.s, a.c.shift, b);
+  const int total = sp.n * a.group;
+  const uint8_t *kbase = a.c.codes[0] + (int64_t)h * a.c.head_stride;
+  const uint8_t *vbase = a.c.codes[1] + (int64_t)h * a.c.head_stride;
+
+  // what this thread loads: 16 bytes of K row kt, words of 4 V rows from vt on
+  const int kt = tid / (D / 16), kc = tid % (D / 16);
+  const int vt = 4 * (tid / (D / 4)), vd = 4 * (tid % (D / 4));
+  const int wtok = wave * (TOK / 8);   // the wave's tokens lie in one group of 16
+
+  // late tiles see the most tokens: they start first
+  const int ntiles = (total + kPromptRows - 1) / kPromptRows;
+  for (int tile = ntiles - 1 - (int)blockIdx.z; tile >= 0; tile -= a.tiles) {
+    const int rho0 = tile * kPromptRows, rho1 = min(rho0 + kPromptRows, total);
+    const TileRange tr = tile_range(a, sp, rho0, rho1);
+    if (split >= max(tr.active, a.splits == 1 ? 1 : 0)) continue;   // nothing here (uniform)
+    const int t0 = tr.start + split * a.chunk;
+    const int t1 = split == a.splits - 1 ? tr.hi : min(tr.hi, t0 + a.chunk);
+
+    // queries: lane (col, half) holds dims 16 k + 8 half + t of query col
+    const int rho = rho0 + 32 * wave + col;
+    const bool mine = rho < rho1;
+    const int qi = (mine ? rho : rho0) / a.group, qh = (mine ? rho : rho0) % a.group;
+    const int pos = mine ? sp.pos0 + qi : -1;
+    u32x4_t qf[KS];
+    float qs;
+    {
+      const uint16_t *qp = a.q + (int64_t)(sp.row0 + qi) * a.q_row +
+                           (int64_t)(h * a.group + qh) * a.q_head + 8 * half;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+        qf[k] = mine ? *reinterpret_cast<const u32x4_t *>(qp + 16 * k) : u32x4_t{0, 0, 0, 0};
+      qs = fabsf(a.scale_log2);
+      if (a.bf16) {
+        float mx = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            mx = fmaxf(mx, fmaxf(__builtin_bit_cast(float, (qf[k][w] << 16) & 0x7FFFFFFFu),
+                                 __builtin_bit_cast(float, qf[k][w] & 0x7FFF0000u)));
+        mx = fmaxf(mx, shfl_x(mx, 32));
+        const int e = (int)(__builtin_bit_cast(uint32_t, mx) >> 23) - 127;
+        const float down = ldexpf(1.f, -(e / 2)), down2 = ldexpf(1.f, -(e - e / 2));
+        qs = qs * ldexpf(1.f, e / 2) * ldexpf(1.f, e - e / 2);
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float lo = __builtin_bit_cast(float, qf[k][w] << 16) * down * down2;
+            const float hi = __builtin_bit_cast(float, qf[k][w] & 0xFFFF0000u) * down * down2;
+            qf[k][w] = h2_bits(f16x2_t{(_Float16)lo, (_Float16)hi});
+          }
+      }
+      // the sign of the scale goes to q, so that score factors are not negative
+      const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) qf[k][w] ^= flip;
+    }
+    // tokens that all of the wave's queries see, and that any of them sees
+    const int wr0 = min(rho0 + 32 * wave, rho1 - 1), wr1 = min(rho0 + 32 * wave + 32, rho1) - 1;
+    const bool wave_on = rho0 + 32 * wave < rho1;
+    const int first_pos = sp.pos0 + wr0 / a.group, last_pos = sp.pos0 + wr1 / a.group;
+    const int all_hi = min(tr.hi, first_pos + 1);
+    const int all_lo = a.window > 0 ? max(tr.lo, last_pos - a.window + 1) : tr.lo;
+    const int any_hi = min(tr.hi, last_pos + 1);
+    const int any_lo = a.window > 0 ? max(tr.lo, first_pos - a.window + 1) : tr.lo;
+
+    f32x16v acc[DT];
+#pragma unroll
+    for (int j = 0; j < DT; ++j) acc[j] = f32x16v{};
+    float m = -FLT_MAX, l = 0.f, unit = 0.f, inv_unit = 0.f;
+
+    u32x4_t kreg;
+    uint32_t vreg[4];
+    float skreg, svreg;
+    auto page_id = [&](int base) {
+      const int tok = (base + wtok) & ~15;   // the group's first: its waves agree
+      return tok < t1 && tok + 16 > tr.lo ? kv_page(a.s, a.c.pages, b, tok >> a.c.shift) : -1;
+    };
+    auto load = [&](int base, int id) {
+      kreg = u32x4_t{0, 0, 0, 0};
+      vreg[0] = vreg[1] = vreg[2] = vreg[3] = 0u;
+      skreg = -1.f;
+      svreg = 0.f;
+      if (id >= 0) {
+        const int64_t page = (int64_t)id * a.c.page_stride;
+        const int mask = (1 << a.c.shift) - 1;
+        kreg = *reinterpret_cast<const u32x4_t *>(
+            kbase + page + (int64_t)((base + kt) & mask) * a.c.token_stride + 16 * kc);
+        const uint8_t *vp = vbase + page + (int64_t)((base + vt) & mask) * a.c.token_stride + vd;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          vreg[t] = *reinterpret_cast<const uint32_t *>(vp + (int64_t)t * a.c.token_stride);
+        skreg = a.c.scales[0][(int64_t)id * a.c.heads + h];
+        svreg = a.c.scales[1][(int64_t)id * a.c.heads + h];
+      }
+    };
+    auto store = [&](int base, int buf) {
+      const u32x2_t c0 = codes4<E4M3>(kreg[0]), c1 = codes4<E4M3>(kreg[1]);
+      const u32x2_t c2 = codes4<E4M3>(kreg[2]), c3 = codes4<E4M3>(kreg[3]);
+      *reinterpret_cast<u32x4_t *>(&k_lds[buf][Tile::k_at(kt, 2 * kc)]) =
+          u32x4_t{c0[0], c0[1], c1[0], c1[1]};
+      *reinterpret_cast<u32x4_t *>(&k_lds[buf][Tile::k_at(kt, 2 * kc + 1)]) =
+          u32x4_t{c2[0], c2[1], c3[0], c3[1]};
+      // rows outside the visible range may hold anything: 0 * NaN
+      if (base + vt < tr.lo || base + vt + 4 > tr.hi) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          if (base + vt + t < tr.lo || base + vt + t >= tr.hi) vreg[t] = 0u;
+      }
+      const int quad = (vt >> 2) & 3, chunk = 2 * (vt >> 4) + (quad & 1), part = 8 * (quad >> 1);
+      *reinterpret_cast<u32x2_t *>(&v_lds[buf][Tile::v_at(vd, chunk) + part]) =
+          u32x2_t{column_pair<E4M3, 0>(vreg[0], vreg[1]), column_pair<E4M3, 0>(vreg[2], vreg[3])};
+      *reinterpret_cast<u32x2_t *>(&v_lds[buf][Tile::v_at(vd + 1, chunk) + part]) =
+          u32x2_t{column_pair<E4M3, 1>(vreg[0], vreg[1]), column_pair<E4M3, 1>(vreg[2], vreg[3])};
+      *reinterpret_cast<u32x2_t *>(&v_lds[buf][Tile::v_at(vd + 2, chunk) + part]) =
+          u32x2_t{column_pair<E4M3, 2>(vreg[0], vreg[1]), column_pair<E4M3, 2>(vreg[2], vreg[3])};
+      *reinterpret_cast<u32x2_t *>(&v_lds[buf][Tile::v_at(vd + 3, chunk) + part]) =
+          u32x2_t{column_pair<E4M3, 3>(vreg[0], vreg[1]), column_pair<E4M3, 3>(vreg[2], vreg[3])};
+      if (lane == 0) {   // waves of one group write the same values
+        sk_lds[buf][wtok >> 4] = skreg;
+        sv_lds[buf][wtok >> 4] = svreg;
+      }
+    };
+
+    int id = page_id(t0), id_next = page_id(t0 + TOK);
+    __syncthreads();   // the previous tile's last readers
+    load(t0, id);
+    store(t0, 0);
+    __syncthreads();
+    for (int base = t0, buf = 0; base < t1; base += TOK, buf ^= 1) {
+      const bool more = base + TOK < t1;
+      if (more) {
+        load(base + TOK, id_next);
+        id_next = page_id(base + 2 * TOK);
+      }
+      if (wave_on && base < any_hi && base + TOK > any_lo) {
+        float f[GR], sv[GR];
+        bool plain = base >= all_lo && base + TOK <= all_hi;
+        float grown = unit;
+#pragma unroll
+        for (int g = 0; g < GR; ++g) {
+          f[g] = sk_lds[buf][g];
+          sv[g] = sv_lds[buf][g];
+          plain = plain && f[g] >= 0.f;
+          grown = fmaxf(grown, sv[g]);
+        }
+        if (__any(grown > unit)) {   // the same in every lane
+          const float c = unit / grown;
+#pragma unroll
+          for (int j = 0; j < DT; ++j) acc[j] *= c;
+          unit = grown;
+          inv_unit = kPUnit / grown;
+        }
+        f32x16v s[TT];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          s[t] = f32x16v{};
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+            s[t] = mfma32h(*reinterpret_cast<const u32x4_t *>(
+                               &k_lds[buf][Tile::k_at(32 * t + col, 2 * k + half)]),
+                           qf[k], s[t]);
+        }
+        // register v of tile t: token 32 t + 8 (v / 4) + 4 half + v % 4, group 2 t + v / 8
+        if (__all(plain)) {
+#pragma unroll
+          for (int g = 0; g < GR; ++g) f[g] *= qs;
+        } else {
+#pragma unroll
+          for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+              const int tok = base + 32 * t + 8 * (v >> 2) + 4 * half + (v & 3);
+              const bool in = f[2 * t + (v >> 3)] >= 0.f && tok <= pos && tok < tr.hi &&
+                              tok >= tr.lo && (a.window <= 0 || tok > pos - a.window);
+              s[t][v] = in ? s[t][v] * (f[2 * t + (v >> 3)] * qs) : -INFINITY;
+            }
+#pragma unroll
+          for (int g = 0; g < GR; ++g) f[g] = 1.f;
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < GR; ++g) {
+          float x = s[g >> 1][8 * (g & 1)];
+#pragma unroll
+          for (int v = 1; v < 8; ++v) x = fmaxf(x, s[g >> 1][8 * (g & 1) + v]);
+          mx = fmaxf(mx, x * f[g]);
+        }
+        if (__any(mx > m)) {
+          const float mn = fmaxf(m, fmaxf(mx, shfl_x(mx, 32)));
+          const float c = exp2_hw(m - mn);
+          l *= c;
+#pragma unroll
+          for (int j = 0; j < DT; ++j) acc[j] *= c;
+          m = mn;
+        }
+#pragma unroll
+        for (int g = 0; g < GR; ++g) {   // one k step of p . v: 16 tokens
+          const float c = sv[g] * inv_unit;
+          float p[8];
+#pragma unroll
+          for (int v = 0; v < 8; ++v) {
+            p[v] = exp2_hw(__builtin_fmaf(s[g >> 1][8 * (g & 1) + v], f[g], -m));
+            l += p[v];
+            p[v] *= c;
+          }
+          u32x4_t pf;
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            pf[w] = h2_bits(f16x2_t{(_Float16)p[2 * w], (_Float16)p[2 * w + 1]});
+#pragma unroll
+          for (int j = 0; j < DT; ++j)
+            acc[j] = mfma32h(*reinterpret_cast<const u32x4_t *>(
+                                 &v_lds[buf][Tile::v_at(32 * j + col, 2 * g + half)]),
+                             pf, acc[j]);
+        }
+      }
+      if (more) store(base + TOK, buf ^ 1);
+      __syncthreads();
+    }
+
+    const float lsum = l + shfl_x(l, 32);
+    if (mine) {
+      const bool none = lsum == 0.f;
+      const float inv = none ? 0.f : unit * (1.f / kPUnit) / lsum;
+      const float lse2 = none ? -INFINITY : m + log2f(lsum);
+      const int64_t row = (int64_t)(sp.row0 + qi) * a.heads_q + h * a.group + qh;
+      if (a.splits == 1) {
+#pragma unroll
+        for (int j = 0; j < DT; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            union {
+              uint16_t e[4];
+              u32x2_t w;
+            } t;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) t.e[v] = to_out(acc[j][4 * i + v] * inv, a.bf16);
+            *reinterpret_cast<u32x2_t *>(a.out + row * D + 32 * j + 8 * i + 4 * half) = t.w;
+          }
+        if (a.lse && half == 0) a.lse[row] = lse2 * kLn2;
+      } else {
+        const int64_t at = (int64_t)split * a.s.rows * a.heads_q + row;
+#pragma unroll
+        for (int j = 0; j < DT; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<f32x4_t *>(a.part_o + at * D + 32 * j + 8 * i + 4 * half) =
+                f32x4_t{acc[j][4 * i] * inv, acc[j][4 * i + 1] * inv, acc[j][4 * i + 2] * inv,
+                        acc[j][4 * i + 3] * inv};
+        if (half == 0) a.part_lse[at] = lse2;
+      }
+    }
+  }
+}
+
 // Joins the splits of each query in split order.  A query whose tile had no
 // token (no split was active) gets 0 and -inf.
-template <int D, int NT>
-__global__ __launch_bounds__(kThreads) void kv_attn_join_kernel(KvAttnArgs a) {
-  constexpr int ROWS = 16 * NT, TPR = D / 4;   // threads per query row
+template <int D>
+__global__ __launch_bounds__(kThreads) void kv_attn_join_kernel(KvAttnArgs a, int ROWS) {
+  constexpr int TPR = D / 4;   // threads per query row
   const int b = blockIdx.x, h = blockIdx.y;
   const KvSpan sp = kv_span(a.s, a.c.shift, b);
   const int total = sp.n * a.group;
@@ -447,29 +763,35 @@ __global__ __launch_bounds__(kThreads) void kv_attn_join_kernel(KvAttnArgs a) {
 }
 
 template <int D, int NT>
-hipError_t launch_nt(const KvAttnArgs &a, bool e4m3, hipStream_t st) {
+void launch_decode(const KvAttnArgs &a, bool e4m3, hipStream_t st) {
   const dim3 grid((unsigned)a.s.batch * (unsigned)a.splits, (unsigned)a.c.heads, (unsigned)a.tiles);
   if (e4m3)
     hipLaunchKernelGGL((kv_attn_kernel<D, true, NT>), grid, dim3(kThreads), 0, st, a);
   else
     hipLaunchKernelGGL((kv_attn_kernel<D, false, NT>), grid, dim3(kThreads), 0, st, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL((kv_attn_join_kernel<D, NT>),
-                     dim3((unsigned)a.s.batch, (unsigned)a.c.heads, (unsigned)a.tiles),
-                     dim3(kThreads), 0, st, a);
-  return hipGetLastError();
+}
+
+template <int D>
+void launch_prompt(const KvAttnArgs &a, bool e4m3, hipStream_t st) {
+  const dim3 grid((unsigned)a.c.heads, (unsigned)a.s.batch * (unsigned)a.splits, (unsigned)a.tiles);
+  if (e4m3)
+    hipLaunchKernelGGL((kv_prompt_kernel<D, true>), grid, dim3(kPromptThreads), 0, st, a);
+  else
+    hipLaunchKernelGGL((kv_prompt_kernel<D, false>), grid, dim3(kPromptThreads), 0, st, a);
 }
 
 template <int D>
 hipError_t launch_dim(const KvAttnArgs &a, bool e4m3, int nt, hipStream_t st) {
-  switch (nt) {
-    case 1: return launch_nt<D, 1>(a, e4m3, st);
-    case 2: return launch_nt<D, 2>(a, e4m3, st);
-    default:
-      if constexpr (D == 256) return launch_nt<D, 2>(a, e4m3, st);
-      else return launch_nt<D, 4>(a, e4m3, st);
-  }
+  if (nt == 0) launch_prompt<D>(a, e4m3, st);
+  else if (nt == 1) launch_decode<D, 1>(a, e4m3, st);
+  else if (nt == 2 || D == 256) launch_decode<D, 2>(a, e4m3, st);
+  else if constexpr (D != 256) launch_decode<D, 4>(a, e4m3, st);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  hipLaunchKernelGGL((kv_attn_join_kernel<D>),
+                     dim3((unsigned)a.s.batch, (unsigned)a.c.heads, (unsigned)a.tiles),
+                     dim3(kThreads), 0, st, a, nt == 0 ? kPromptRows : 16 * nt);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -480,14 +802,15 @@ KvAttnPlan kv_attn_plan(int batch, int heads, int dim, int64_t capacity, int64_t
   const int64_t group = heads_q / heads;
   const int64_t q = std::min(max_q, rows);
   const int64_t qrows = q * group;
-  p.nt = qrows <= 16 ? 1 : qrows <= 32 || dim == 256 ? 2 : 4;
-  p.tiles = (int)std::min<int64_t>((qrows + 16 * p.nt - 1) / (16 * p.nt), 65535);
+  p.nt = qrows <= 16 ? 1 : qrows <= 32 || (dim == 256 && qrows <= 64) ? 2 : qrows <= 64 ? 4 : 0;
+  const int tile_rows = p.nt == 0 ? kPromptRows : 16 * p.nt;
+  p.tiles = (int)std::min<int64_t>((qrows + tile_rows - 1) / tile_rows, 65535);
   int64_t span = std::min(max_len, capacity);
-  if (window > 0) span = std::min<int64_t>(span, (int64_t)window + 16 * p.nt / group + 1);
+  if (window > 0) span = std::min<int64_t>(span, (int64_t)window + tile_rows / group + 1);
   span += kBlock - 1;   // a range may start up to 31 tokens before its first visible one
   const int64_t base = (int64_t)batch * heads * p.tiles;
-  constexpr int64_t kStep = kBlock * kWaves;   // one step of every wave
-  constexpr int64_t kTarget = 2048;            // workgroups that fill the chip several times
+  const int64_t kStep = p.nt == 0 ? 8192 / dim : kBlock * kWaves;   // one step of every wave
+  const int64_t kTarget = p.nt == 0 ? 512 : 2048;   // workgroups that fill the chip
   int64_t splits = std::max<int64_t>(1, std::min<int64_t>(kTarget / base, (span + kStep - 1) / kStep));
   splits = std::min<int64_t>(splits, 256);
   const int64_t chunk = ((span + splits - 1) / splits + kStep - 1) / kStep * kStep;

@@ -20,7 +20,7 @@ hipError_t launch_kv_read(const KvView &c, const SeqView &s, bool e4m3, void *k,
 
 // kv_attention.hip
 struct KvAttnPlan {
-  int nt;         // 16-query tiles per workgroup
+  int nt;         // 16-query tiles per workgroup of the decode kernel; 0: prompt kernel
   int tiles;      // workgroups along a sequence's query rows
   int splits;     // workgroups along the tokens
   int chunk;      // tokens per split (the last split takes the rest)

@@ -12,7 +12,7 @@
 namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30;     // rows * heads, and cached tokens per sequence
-constexpr int64_t kMaxBatch = 65536;
+constexpr int64_t kMaxBatch = 65535;
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
