@@ -41,7 +41,8 @@ typedef enum { SLQ_F32 = 0, SLQ_BF16 = 1, SLQ_F16 = 2 } slq_dtype;
  * head_dim is 64, 128 or 256 (else SLQ_ENOTSUP), page_size a power of two in
  * 16..256 (else SLQ_ENOTSUP), heads in 1..1024.  Strides are in bytes,
  * multiples of 16, and must not make two (page, head, slot) rows overlap:
- * either heads outside slots or slots outside heads within a page.
+ * either heads outside slots or slots outside heads within a page, which
+ * spans less than 2^31 bytes.
  * Alignment: codes 16 bytes, scales 4 bytes.
  */
 typedef struct {
@@ -132,7 +133,7 @@ size_t slq_kv_attention_workspace_bytes(const slq_kv_cache *cache, const slq_kv_
  * Scores, softmax sums and outputs accumulate in fp32; codes enter the matrix
  * units exactly, q after an exact shift of its exponent (elements below 2^-17
  * of their row's largest round to 2^-25 of it), probabilities rounded to
- * binary16 with 15 bits of headroom below the largest.
+ * binary16, each to 2^-12 of itself or 2^-36 of the weight of the largest.
  * max_q, max_len: the largest n_b and lens[b] the caller expects; they choose
  * the kernel and its grid, results are right for any values >= 1.
  * workspace: as sized above, 256-byte aligned, overwritten; NULL when 0.

@@ -5,9 +5,11 @@ Bounds of attention, per output (R = rounding of the output type, eps / 2):
   score error  e = 2^-24 (dim + 8) S + 2^-22 |lse| + 2^-20, S = max_j scale sum |q||k_j|
     (fp32 accumulation of exact products, one rounding of the factors, of the
     shift by the running maximum and of the base-2 exponential each);
-  |out - ref| <= (2^-11 + 2.5 e) A + R (|ref| + (2^-11 + 2.5 e) A) + 2^-38 max|v|, A = sum_j p_j |v_j|
+  |out - ref| <= (2^-11 + 2.5 e) A + R (|ref| + (2^-11 + 2.5 e) A) + 2^-24 max|v|, A = sum_j p_j |v_j|
     (2^-11: a probability in binary16; p / sum p moves by at most 2 e relative;
-    2^-38: n <= 4096 probabilities below 2^-39 of the largest lose up to 2^-50 each);
+    2^-24: probabilities are held times 2^11 in binary16, whose subnormals are
+    2^-24 apart, so each of n <= 4096 loses at most 2^-25 / 2^11 = 2^-36 of a weight
+    of 1, in units of the largest page scale times the largest code);
     (an output below 2^-14 is a binary16 subnormal, whose spacing is 2^-24 whatever
     its size: rounding to fp16 adds up to 2^-25 there, beside the relative R);
   |lse - ref| <= e."""
@@ -227,7 +229,7 @@ def check_attention(box, table, lens, cu, q, window=0, scale=None, max_q=None, m
         rel = 2.0 ** -11 + 2.5 * e[on][:, None]
         R = torch.finfo(q.dtype).eps / 2
         vmax = 448 * np.nanmax(np.abs(box.scales[1]))
-        bound = rel * A[on] + R * (np.abs(ro[on]) + rel * A[on]) + 2.0 ** -38 * vmax
+        bound = rel * A[on] + R * (np.abs(ro[on]) + rel * A[on]) + 2.0 ** -24 * vmax
         if q.dtype == torch.float16:
             bound += 2.0 ** -25
         err = np.abs(got[on] - ro[on])

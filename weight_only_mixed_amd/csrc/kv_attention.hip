@@ -21,9 +21,13 @@
 // tokens of its slots; the byte transposition is part of the conversion.
 // Nothing passes through shared memory before the epilogue.
 //
-// Probabilities enter the second product as binary16 of p * 2^15 * sv / R with
-// R the largest sv met so far (folded into the accumulator when it grows):
-// values down to 2^-39 of the largest still count.
+// Probabilities are taken relative to a reference m that a score has reached,
+// and that follows the running maximum only when that has risen by more than
+// 2^4 (otherwise some query of a tile has a new maximum nearly every time, and
+// all accumulators would be rescaled for a change of no consequence).  They
+// enter the second product as binary16 of p * 2^11 * sv / R with R the largest
+// sv met so far (folded into the accumulator when it grows): at most 2^15, and
+// each loses at most 2^-36 of m's weight where binary16 runs out of exponent.
 #include <float.h>
 
 #include <algorithm>
@@ -41,7 +45,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kBlock = 32;            // tokens per wave and step
-constexpr float kPUnit = 32768.f;     // probabilities are held times this
+constexpr float kPUnit = 2048.f;      // probabilities are held times this
+constexpr float kSlack = 4.f;         // and may reach 2^kSlack
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float exp2_hw(float v) { return __builtin_amdgcn_exp2f(v); }
@@ -68,8 +73,10 @@ __device__ __forceinline__ u32x2_t codes4(uint32_t w) {
     r[0] = h2_bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, 1.0f, false));
     r[1] = h2_bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, 1.0f, true));
   } else {
-    r[0] = int8_pair(perm(0u, w, 0x0c010c00u));
-    r[1] = int8_pair(perm(0u, w, 0x0c030c02u));
+    const f16x2_t bias = {(_Float16)1152.f, (_Float16)1152.f};
+    const uint32_t u = w ^ 0x80808080u;   // b + 128; 0x64 above it makes 1024 + (b + 128)
+    r[0] = h2_bits(__builtin_bit_cast(f16x2_t, perm(0x64646464u, u, 0x04010400u)) - bias);
+    r[1] = h2_bits(__builtin_bit_cast(f16x2_t, perm(0x64646464u, u, 0x04030402u)) - bias);
   }
   return r;
 }
@@ -203,7 +210,7 @@ __global__ __launch_bounds__(kThreads) void kv_attn_kernel(KvAttnArgs a) {
 #pragma unroll
       for (int j = 0; j < VJ; ++j) acc[n][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
-    float unit = 0.f, inv_unit = 0.f;   // R and 2^15 / R
+    float unit = 0.f, inv_unit = 0.f;   // R and kPUnit / R
     // tokens every query of this tile sees
     const int all_hi = min(tr.hi, sp.pos0 + rho0 / a.group + 1);
     const int last_pos = sp.pos0 + (rho1 - 1) / a.group;
@@ -315,7 +322,7 @@ __global__ __launch_bounds__(kThreads) void kv_attn_kernel(KvAttnArgs a) {
         float mx = s[n][0][0];
 #pragma unroll
         for (int v = 1; v < 8; ++v) mx = fmaxf(mx, s[n][v >> 2][v & 3]);
-        if (__any(mx > m[n])) {
+        if (__any(mx > m[n] + kSlack)) {
           const float mn = fmaxf(m[n], quad_max(mx));
           const float f = exp2_hw(m[n] - mn);
           l[n] *= f;
@@ -471,6 +478,15 @@ __global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs
   const int kt = tid / (D / 16), kc = tid % (D / 16);
   const int vt = 4 * (tid / (D / 4)), vd = 4 * (tid % (D / 4));
   const int wtok = wave * (TOK / 8);   // the wave's tokens lie in one group of 16
+  // offsets from the wave's first row: the same for every tile
+  const uint32_t koff = (uint32_t)((kt - wtok) * (int)a.c.token_stride + 16 * kc);
+  const uint32_t voff = (uint32_t)((vt - wtok) * (int)a.c.token_stride + vd);
+  // where the converted codes go (in_vgpr: kept, not recomputed every tile)
+  const int quad = (vt >> 2) & 3, chunk = 2 * (vt >> 4) + (quad & 1), part = 8 * (quad >> 1);
+  const uint32_t kdst0 = in_vgpr(Tile::k_at(kt, 2 * kc)), kdst1 = in_vgpr(Tile::k_at(kt, 2 * kc + 1));
+  uint32_t vdst[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) vdst[c] = in_vgpr(Tile::v_at(vd + c, chunk) + part);
 
   // late tiles see the most tokens: they start first
   const int ntiles = (total + kPromptRows - 1) / kPromptRows;
@@ -550,14 +566,13 @@ __global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs
       skreg = -1.f;
       svreg = 0.f;
       if (id >= 0) {
-        const int64_t page = (int64_t)id * a.c.page_stride;
-        const int mask = (1 << a.c.shift) - 1;
-        kreg = *reinterpret_cast<const u32x4_t *>(
-            kbase + page + (int64_t)((base + kt) & mask) * a.c.token_stride + 16 * kc);
-        const uint8_t *vp = vbase + page + (int64_t)((base + vt) & mask) * a.c.token_stride + vd;
+        const int slot = (base + wtok) & ((1 << a.c.shift) - 1);
+        const int64_t at = (int64_t)id * a.c.page_stride + (int64_t)slot * a.c.token_stride;
+        kreg = *reinterpret_cast<const u32x4_t *>(kbase + at + koff);
+        const uint8_t *vp = vbase + at;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-          vreg[t] = *reinterpret_cast<const uint32_t *>(vp + (int64_t)t * a.c.token_stride);
+        for (int t = 0; t < 4; ++t, vp += a.c.token_stride)
+          vreg[t] = *reinterpret_cast<const uint32_t *>(vp + voff);
         skreg = a.c.scales[0][(int64_t)id * a.c.heads + h];
         svreg = a.c.scales[1][(int64_t)id * a.c.heads + h];
       }
@@ -565,24 +580,23 @@ __global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs
     auto store = [&](int base, int buf) {
       const u32x2_t c0 = codes4<E4M3>(kreg[0]), c1 = codes4<E4M3>(kreg[1]);
       const u32x2_t c2 = codes4<E4M3>(kreg[2]), c3 = codes4<E4M3>(kreg[3]);
-      *reinterpret_cast<u32x4_t *>(&k_lds[buf][Tile::k_at(kt, 2 * kc)]) =
+      *reinterpret_cast<u32x4_t *>(&k_lds[buf][kdst0]) =
           u32x4_t{c0[0], c0[1], c1[0], c1[1]};
-      *reinterpret_cast<u32x4_t *>(&k_lds[buf][Tile::k_at(kt, 2 * kc + 1)]) =
+      *reinterpret_cast<u32x4_t *>(&k_lds[buf][kdst1]) =
           u32x4_t{c2[0], c2[1], c3[0], c3[1]};
       // rows outside the visible range may hold anything: 0 * NaN
-      if (base + vt < tr.lo || base + vt + 4 > tr.hi) {
+      if (base + wtok < tr.lo || base + wtok + TOK / 8 > tr.hi) {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
           if (base + vt + t < tr.lo || base + vt + t >= tr.hi) vreg[t] = 0u;
       }
-      const int quad = (vt >> 2) & 3, chunk = 2 * (vt >> 4) + (quad & 1), part = 8 * (quad >> 1);
-      *reinterpret_cast<u32x2_t *>(&v_lds[buf][Tile::v_at(vd, chunk) + part]) =
+      *reinterpret_cast<u32x2_t *>(&v_lds[buf][vdst[0]]) =
           u32x2_t{column_pair<E4M3, 0>(vreg[0], vreg[1]), column_pair<E4M3, 0>(vreg[2], vreg[3])};
-      *reinterpret_cast<u32x2_t *>(&v_lds[buf][Tile::v_at(vd + 1, chunk) + part]) =
+      *reinterpret_cast<u32x2_t *>(&v_lds[buf][vdst[1]]) =
           u32x2_t{column_pair<E4M3, 1>(vreg[0], vreg[1]), column_pair<E4M3, 1>(vreg[2], vreg[3])};
-      *reinterpret_cast<u32x2_t *>(&v_lds[buf][Tile::v_at(vd + 2, chunk) + part]) =
+      *reinterpret_cast<u32x2_t *>(&v_lds[buf][vdst[2]]) =
           u32x2_t{column_pair<E4M3, 2>(vreg[0], vreg[1]), column_pair<E4M3, 2>(vreg[2], vreg[3])};
-      *reinterpret_cast<u32x2_t *>(&v_lds[buf][Tile::v_at(vd + 3, chunk) + part]) =
+      *reinterpret_cast<u32x2_t *>(&v_lds[buf][vdst[3]]) =
           u32x2_t{column_pair<E4M3, 3>(vreg[0], vreg[1]), column_pair<E4M3, 3>(vreg[2], vreg[3])};
       if (lane == 0) {   // waves of one group write the same values
         sk_lds[buf][wtok >> 4] = skreg;
@@ -619,15 +633,29 @@ __global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs
           unit = grown;
           inv_unit = kPUnit / grown;
         }
+        // operand reads run kAhead products ahead: the compiler left alone reads
+        // each operand right before its product and waits the whole read out
+        constexpr int kAhead = 4, NS = KS * TT, NP = GR * DT;
+        u32x4_t op[kAhead];
+        auto k_op = [&](int i) {
+          return *reinterpret_cast<const u32x4_t *>(
+              &k_lds[buf][Tile::k_at(32 * (i % TT) + col, 2 * (i / TT) + half)]);
+        };
+        auto v_op = [&](int i) {
+          return *reinterpret_cast<const u32x4_t *>(
+              &v_lds[buf][Tile::v_at(32 * (i % DT) + col, 2 * (i / DT) + half)]);
+        };
         f32x16v s[TT];
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          s[t] = f32x16v{};
+        for (int t = 0; t < TT; ++t) s[t] = f32x16v{};
 #pragma unroll
-          for (int k = 0; k < KS; ++k)
-            s[t] = mfma32h(*reinterpret_cast<const u32x4_t *>(
-                               &k_lds[buf][Tile::k_at(32 * t + col, 2 * k + half)]),
-                           qf[k], s[t]);
+        for (int i = 0; i < kAhead; ++i) op[i] = k_op(i);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          s[i % TT] = mfma32h(op[i % kAhead], qf[i / TT], s[i % TT]);
+          op[i % kAhead] = i + kAhead < NS ? k_op(i + kAhead) : v_op(i + kAhead - NS);
+          __builtin_amdgcn_sched_barrier(0);
         }
         // register v of tile t: token 32 t + 8 (v / 4) + 4 half + v % 4, group 2 t + v / 8
         if (__all(plain)) {
@@ -654,7 +682,7 @@ __global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs
           for (int v = 1; v < 8; ++v) x = fmaxf(x, s[g >> 1][8 * (g & 1) + v]);
           mx = fmaxf(mx, x * f[g]);
         }
-        if (__any(mx > m)) {
+        if (__any(mx > m + kSlack)) {
           const float mn = fmaxf(m, fmaxf(mx, shfl_x(mx, 32)));
           const float c = exp2_hw(m - mn);
           l *= c;
@@ -662,8 +690,9 @@ __global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs
           for (int j = 0; j < DT; ++j) acc[j] *= c;
           m = mn;
         }
+        u32x4_t pf[GR];   // one k step of p . v per group of 16 tokens
 #pragma unroll
-        for (int g = 0; g < GR; ++g) {   // one k step of p . v: 16 tokens
+        for (int g = 0; g < GR; ++g) {
           const float c = sv[g] * inv_unit;
           float p[8];
 #pragma unroll
@@ -672,15 +701,16 @@ __global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs
             l += p[v];
             p[v] *= c;
           }
-          u32x4_t pf;
 #pragma unroll
           for (int w = 0; w < 4; ++w)
-            pf[w] = h2_bits(f16x2_t{(_Float16)p[2 * w], (_Float16)p[2 * w + 1]});
+            pf[g][w] = h2_bits(f16x2_t{(_Float16)p[2 * w], (_Float16)p[2 * w + 1]});
+        }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int j = 0; j < DT; ++j)
-            acc[j] = mfma32h(*reinterpret_cast<const u32x4_t *>(
-                                 &v_lds[buf][Tile::v_at(32 * j + col, 2 * g + half)]),
-                             pf, acc[j]);
+        for (int i = 0; i < NP; ++i) {
+          acc[i % DT] = mfma32h(op[i % kAhead], pf[i / DT], acc[i % DT]);
+          if (i + kAhead < NP) op[i % kAhead] = v_op(i + kAhead);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
       if (more) store(base + TOK, buf ^ 1);

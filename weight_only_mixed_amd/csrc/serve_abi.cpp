@@ -65,6 +65,7 @@ slq_status check_cache(const slq_kv_cache *c, slq::KvView *v, CacheExtents *x) {
                              ts >= (c->heads - 1) * hs + c->head_dim;
   if (!heads_outside && !slots_outside) return SLQ_EINVAL;
   const int64_t span = page_span(c);
+  if (span >= ((int64_t)1 << 31)) return SLQ_EINVAL;   // offsets within a page fit 32 bits
   if (c->pages > 1 && (ps < span || ps > ((int64_t)1 << 60) / c->pages)) return SLQ_EINVAL;
   *x = CacheExtents{};
   if (c->pages > 0) {
