@@ -335,6 +335,21 @@ def test_attention_ranges(dtype):
     check_attention(zero, table, lens, cu, q.to(T[dtype]), what="zero scales")
 
 
+@pytest.mark.parametrize("new", [1, 40])
+def test_attention_not_a_number(new):
+    """A query of NaN gives NaN in its own row and head only, split or not."""
+    g = np.random.default_rng(3)
+    box = Box(40, 1, 128, 16, "int8", seed=2, fill="values")
+    q = rand(g, (new, 4, 128), "bf16")
+    q[0, 1, 5] = float("nan")
+    for max_len in (1, 600):
+        o, lse = slq.slq_kv_attention(box.dev, gseqs(np.arange(40)[None], [600], [0, new]), q, max_q=new, max_len=max_len,
+                                      with_lse=True)
+        bad = torch.isnan(o.float()).all(2)
+        assert bool(bad[0, 1]) and int(bad.sum()) == 1 and not bool(torch.isnan(o.float()).any(2)[~bad].any())
+        assert bool(torch.isnan(lse[0, 1])) and int(torch.isnan(lse).sum()) == 1
+
+
 def test_attention_strided_queries():
     g = np.random.default_rng(6)
     box = Box(4, 2, 64, 32, "e4m3", seed=2, fill="values")

@@ -22,7 +22,9 @@ EXTRA = {"quantize.hip": ["-ffp-contract=off"],
          "gptq.hip": ["-ffp-contract=off"],
          # cache codes are bit-exact IEEE, as the weight codes are
          "kv_cache.hip": ["-ffp-contract=off"],
-         # MFMA results in VGPRs: the decode epilogue reads them with plain VALU ops
+         # MFMA results in VGPRs: the decode epilogue, and attention's softmax and
+         # rescaling, read them with plain VALU ops
+         "kv_attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
          "gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 SOURCES = ["quantize.hip", "gemv.hip", "gemm.hip", "fidelity.hip", "mckp.hip", "gptq.hip", "probe.hip",
            "noalloc.hip", "kv_cache.hip", "kv_attention.hip", "sample.hip",

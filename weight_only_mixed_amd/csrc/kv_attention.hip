@@ -129,8 +129,10 @@ __device__ __forceinline__ TileRange tile_range(const KvAttnArgs &a, const KvSpa
   return t;
 }
 
+// Four waves per SIMD for single tokens: what hides the loads is waves, not
+// blocks in flight per wave.
 template <int D, bool E4M3, int NT>
-__global__ __launch_bounds__(kThreads) void kv_attn_kernel(KvAttnArgs a) {
+__global__ __launch_bounds__(kThreads, (D <= 128 && NT == 1 ? 4 : 1)) void kv_attn_kernel(KvAttnArgs a) {
   constexpr int KS = D / 32;      // MFMA k steps of q . k
   constexpr int VJ = D / 16;      // bytes of a V row per lane, and MFMAs of p . v
   constexpr int KL = D / 64;      // 16-byte K loads per token and lane
@@ -149,6 +151,9 @@ __global__ __launch_bounds__(kThreads) void kv_attn_kernel(KvAttnArgs a) {
   const int total = sp.n * a.group;
   const uint8_t *kbase = a.c.codes[0] + (int64_t)h * a.c.head_stride;
   const uint8_t *vbase = a.c.codes[1] + (int64_t)h * a.c.head_stride;
+  // lane offsets into a 16-token tile: 16 bytes of K row col, V rows 4 g ..
+  const uint32_t koff = (uint32_t)(col * (int)a.c.token_stride + 16 * g);
+  const uint32_t voff = (uint32_t)(4 * g * (int)a.c.token_stride + VJ * col);
 
   for (int rho0 = blockIdx.z * ROWS; rho0 < total; rho0 += a.tiles * ROWS) {
     const int rho1 = min(rho0 + ROWS, total);
@@ -216,53 +221,67 @@ __global__ __launch_bounds__(kThreads) void kv_attn_kernel(KvAttnArgs a) {
     const int last_pos = sp.pos0 + (rho1 - 1) / a.group;
     const int all_lo = a.window > 0 ? max(tr.lo, last_pos - a.window + 1) : tr.lo;
 
-    for (int blk = t0 + kBlock * wave; blk < t1; blk += kBlock * kWaves) {
-      // the two 16-token tiles: their pages (a tile never crosses a page)
+    // the two 16-token tiles of a wave's step: their pages (a tile never crosses
+    // a page), scales and codes
+    struct Block {
       int id[2];
       float sk[2], sv[2];
       u32x4_t kw[2][KL];
       uint32_t vw[2][4][VW];
-      bool plain = blk >= all_lo && blk + kBlock <= all_hi;
+    };
+    // A tile wholly outside the visible range is not looked at: its page may
+    // belong to someone else by now.  Page numbers are read a step ahead.
+    auto page_ids = [&](int blk, int (&id)[2]) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int tok = blk + 16 * u;
-        // a tile wholly outside the visible range is not looked at: its page may
-        // belong to someone else by now
-        id[u] = tok < tr.hi && tok + 16 > tr.lo ? kv_page(a.s, a.c.pages, b, tok >> a.c.shift) : -1;
-        plain = plain && id[u] >= 0;
-        const int64_t at = (int64_t)max(id[u], 0) * a.c.page_stride +
-                           (int64_t)(tok & ((1 << a.c.shift) - 1)) * a.c.token_stride;
-        sk[u] = sv[u] = 0.f;
-        if (id[u] >= 0) {
-          sk[u] = a.c.scales[0][(int64_t)id[u] * a.c.heads + h];
-          sv[u] = a.c.scales[1][(int64_t)id[u] * a.c.heads + h];
-          const uint8_t *kp = kbase + at + (int64_t)col * a.c.token_stride + 16 * g;
-          const uint8_t *vp = vbase + at + (int64_t)(4 * g) * a.c.token_stride + VJ * col;
+        id[u] = tok < t1 && tok < tr.hi && tok + 16 > tr.lo
+                    ? kv_page(a.s, a.c.pages, b, tok >> a.c.shift) : -1;
+      }
+    };
+    auto load = [&](int blk, const int (&id)[2], Block &x) {
 #pragma unroll
-          for (int k = 0; k < KL; ++k) kw[u][k] = *reinterpret_cast<const u32x4_t *>(kp + 64 * k);
+      for (int u = 0; u < 2; ++u) {
+        const int tok = blk + 16 * u;
+        x.id[u] = __builtin_amdgcn_readfirstlane(id[u]);
+        x.sk[u] = x.sv[u] = 0.f;
+        if (x.id[u] >= 0) {
+          const int64_t at = (int64_t)x.id[u] * a.c.page_stride +
+                             (int64_t)(tok & ((1 << a.c.shift) - 1)) * a.c.token_stride;
+          x.sk[u] = a.c.scales[0][(int64_t)x.id[u] * a.c.heads + h];
+          x.sv[u] = a.c.scales[1][(int64_t)x.id[u] * a.c.heads + h];
+          const uint8_t *kp = kbase + at, *vp = vbase + at;
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const uint8_t *row = vp + (int64_t)t * a.c.token_stride;
-            if constexpr (VW == 1) vw[u][t][0] = *reinterpret_cast<const uint32_t *>(row);
+          for (int k = 0; k < KL; ++k) x.kw[u][k] = *reinterpret_cast<const u32x4_t *>(kp + koff + 64 * k);
+#pragma unroll
+          for (int t = 0; t < 4; ++t, vp += a.c.token_stride) {
+            if constexpr (VW == 1) x.vw[u][t][0] = *reinterpret_cast<const uint32_t *>(vp + voff);
             else if constexpr (VW == 2) {
-              const u32x2_t w = *reinterpret_cast<const u32x2_t *>(row);
-              vw[u][t][0] = w[0];
-              vw[u][t][1] = w[1];
+              const u32x2_t w = *reinterpret_cast<const u32x2_t *>(vp + voff);
+              x.vw[u][t][0] = w[0];
+              x.vw[u][t][1] = w[1];
             } else {
-              const u32x4_t w = *reinterpret_cast<const u32x4_t *>(row);
+              const u32x4_t w = *reinterpret_cast<const u32x4_t *>(vp + voff);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) vw[u][t][i] = w[i];
+              for (int i = 0; i < 4; ++i) x.vw[u][t][i] = w[i];
             }
           }
         } else {
 #pragma unroll
-          for (int k = 0; k < KL; ++k) kw[u][k] = u32x4_t{0, 0, 0, 0};
+          for (int k = 0; k < KL; ++k) x.kw[u][k] = u32x4_t{0, 0, 0, 0};
 #pragma unroll
           for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int i = 0; i < VW; ++i) vw[u][t][i] = 0u;
+            for (int i = 0; i < VW; ++i) x.vw[u][t][i] = 0u;
         }
       }
+    };
+    auto step = [&](int blk, Block &x) {
+      const int (&id)[2] = x.id;
+      const float (&sk)[2] = x.sk, (&sv)[2] = x.sv;
+      const u32x4_t (&kw)[2][KL] = x.kw;
+      uint32_t (&vw)[2][4][VW] = x.vw;
+      const bool plain = blk >= all_lo && blk + kBlock <= all_hi && id[0] >= 0 && id[1] >= 0;
       if (!plain) {   // rows outside every query's range may hold anything: 0 * NaN
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -351,6 +370,16 @@ __global__ __launch_bounds__(kThreads) void kv_attn_kernel(KvAttnArgs a) {
         for (int n = 0; n < NT; ++n) acc[n][J] = mfma16h(vf, pf[n], acc[n][J]);
       };
       for_each_int(column, std::make_integer_sequence<int, VJ>());
+    };
+    // (a second block in flight per wave costs more occupancy than it hides:
+    // 237 us against 188 for 64 sequences of up to 8192 tokens)
+    int id[2];
+    page_ids(t0 + kBlock * wave, id);
+    for (int blk = t0 + kBlock * wave; blk < t1; blk += kBlock * kWaves) {
+      Block x;
+      load(blk, id, x);
+      page_ids(blk + kBlock * kWaves, id);
+      step(blk, x);
     }
 
     // the four waves' parts of each query, joined in wave order
@@ -752,42 +781,78 @@ __global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs
   }
 }
 
-// Joins the splits of each query in split order.  A query whose tile had no
-// token (no split was active) gets 0 and -inf.
+// Joins the splits of each query row: one workgroup per row, the splits dealt to
+// its four waves (fixed sums: split order within a wave, then wave order).  A
+// row whose tile had no token (no split was active) gets 0 and -inf.
 template <int D>
-__global__ __launch_bounds__(kThreads) void kv_attn_join_kernel(KvAttnArgs a, int ROWS) {
-  constexpr int TPR = D / 4;   // threads per query row
+__global__ __launch_bounds__(kThreads) void kv_attn_join_kernel(KvAttnArgs a, int tile_rows) {
+  constexpr int PER = D / kWave;   // outputs per lane
+  constexpr int kU = 8;            // splits in flight per wave
+  __shared__ float o_lds[kWaves][D];
+  __shared__ float m_lds[kWaves], l_lds[kWaves];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int b = blockIdx.x, h = blockIdx.y;
   const KvSpan sp = kv_span(a.s, a.c.shift, b);
   const int total = sp.n * a.group;
-  for (int rho0 = blockIdx.z * ROWS; rho0 < total; rho0 += a.tiles * ROWS) {
-    const int rho1 = min(rho0 + ROWS, total);
-    const TileRange tr = tile_range(a, sp, rho0, rho1);
-    for (int rho = rho0 + threadIdx.x / TPR; rho < rho1; rho += kThreads / TPR) {
-      const int d0 = (threadIdx.x % TPR) * 4;
-      const int i = rho / a.group, hd = rho % a.group;
-      const int64_t row = (int64_t)(sp.row0 + i) * a.heads_q + h * a.group + hd;
-      const int64_t step = (int64_t)a.s.rows * a.heads_q;
-      float m = -INFINITY;
-      for (int s = 0; s < tr.active; ++s) m = fmaxf(m, a.part_lse[s * step + row]);
-      float lsum = 0.f;
-      f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-      if (m != -INFINITY)
-        for (int s = 0; s < tr.active; ++s) {
-          const float e = a.part_lse[s * step + row];
-          const float f = e == -INFINITY ? 0.f : exp2_hw(e - m);
-          lsum += f;
-          o += *reinterpret_cast<const f32x4_t *>(a.part_o + (s * step + row) * D + d0) * f;
-        }
-      const float inv = lsum > 0.f ? 1.f / lsum : lsum == 0.f ? 0.f : lsum;
-      union {
-        uint16_t e[4];
-        u32x2_t w;
-      } t;
+  const int64_t step = (int64_t)a.s.rows * a.heads_q;
+  for (int rho = blockIdx.z; rho < total; rho += gridDim.z) {
+    const int rho0 = rho / tile_rows * tile_rows;
+    const TileRange tr = tile_range(a, sp, rho0, min(rho0 + tile_rows, total));
+    const int i = rho / a.group, hd = rho % a.group;
+    const int64_t row = (int64_t)(sp.row0 + i) * a.heads_q + h * a.group + hd;
+    float m = -INFINITY, l = 0.f, o[PER] = {};
+    for (int base = wave; base < tr.active; base += kU * kWaves) {
+      float e[kU], x[kU][PER];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) t.e[j] = to_out(o[j] * inv, a.bf16);
-      *reinterpret_cast<u32x2_t *>(a.out + row * D + d0) = t.w;
-      if (a.lse && d0 == 0) a.lse[row] = lsum == 0.f ? -INFINITY : (m + log2f(lsum)) * kLn2;
+      for (int u = 0; u < kU; ++u) {
+        const int s = base + u * kWaves;
+        const int64_t at = min(s, tr.active - 1) * step + row;
+        e[u] = s < tr.active ? a.part_lse[at] : -INFINITY;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) x[u][j] = a.part_o[at * D + lane * PER + j];
+      }
+      float top = m;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) top = fmaxf(top, e[u]);
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (e[u] != e[u]) l = e[u];   // a maximum does not show it
+      if (top == -INFINITY) continue;
+      const float f = exp2_hw(m - top);
+      l *= f;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) o[j] *= f;
+      m = top;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const float w = exp2_hw(e[u] - m);   // NaN where the split's sum was
+        l += w;
+        if (e[u] != -INFINITY)
+#pragma unroll
+          for (int j = 0; j < PER; ++j) o[j] += w * x[u][j];
+      }
+    }
+    __syncthreads();   // the previous row's readers
+    if (lane == 0) {
+      m_lds[wave] = m;
+      l_lds[wave] = l;
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j) o_lds[wave][lane * PER + j] = o[j];
+    __syncthreads();
+    float top = m_lds[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, m_lds[w]);
+    for (int d = threadIdx.x; d < D; d += kThreads) {
+      float lsum = 0.f, v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = m_lds[w] == -INFINITY && l_lds[w] == 0.f ? 0.f : exp2_hw(m_lds[w] - top);
+        lsum += f * l_lds[w];
+        v += f * o_lds[w][d];
+      }
+      a.out[row * D + d] = to_out(lsum == 0.f ? 0.f : v / lsum, a.bf16);
+      if (a.lse && d == 0) a.lse[row] = lsum == 0.f ? -INFINITY : (top + log2f(lsum)) * kLn2;
     }
   }
 }
@@ -818,9 +883,11 @@ hipError_t launch_dim(const KvAttnArgs &a, bool e4m3, int nt, hipStream_t st) {
   else if constexpr (D != 256) launch_decode<D, 4>(a, e4m3, st);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
+  const int tile_rows = nt == 0 ? kPromptRows : 16 * nt;
   hipLaunchKernelGGL((kv_attn_join_kernel<D>),
-                     dim3((unsigned)a.s.batch, (unsigned)a.c.heads, (unsigned)a.tiles),
-                     dim3(kThreads), 0, st, a, nt == 0 ? kPromptRows : 16 * nt);
+                     dim3((unsigned)a.s.batch, (unsigned)a.c.heads,
+                          (unsigned)std::min<int64_t>(a.join_rows, 65535)),
+                     dim3(kThreads), 0, st, a, tile_rows);
   return hipGetLastError();
 }
 
@@ -832,6 +899,7 @@ KvAttnPlan kv_attn_plan(int batch, int heads, int dim, int64_t capacity, int64_t
   const int64_t group = heads_q / heads;
   const int64_t q = std::min(max_q, rows);
   const int64_t qrows = q * group;
+  p.rows = (int)std::min<int64_t>(qrows, 65535);
   p.nt = qrows <= 16 ? 1 : qrows <= 32 || (dim == 256 && qrows <= 64) ? 2 : qrows <= 64 ? 4 : 0;
   const int tile_rows = p.nt == 0 ? kPromptRows : 16 * p.nt;
   p.tiles = (int)std::min<int64_t>((qrows + tile_rows - 1) / tile_rows, 65535);
@@ -856,6 +924,7 @@ hipError_t launch_kv_attention(KvAttnArgs a, bool e4m3, const KvAttnPlan &plan, 
   a.splits = plan.splits;
   a.chunk = plan.chunk;
   a.tiles = plan.tiles;
+  a.join_rows = plan.rows;
   a.part_o = static_cast<float *>(ws);
   a.part_lse = plan.splits > 1
                    ? a.part_o + (size_t)plan.splits * a.s.rows * a.heads_q * a.c.dim

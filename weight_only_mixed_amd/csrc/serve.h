@@ -24,6 +24,7 @@ struct KvAttnPlan {
   int tiles;      // workgroups along a sequence's query rows
   int splits;     // workgroups along the tokens
   int chunk;      // tokens per split (the last split takes the rest)
+  int rows;       // query rows per kv head and sequence, as expected
   size_t ws_bytes;
 };
 KvAttnPlan kv_attn_plan(int batch, int heads, int dim, int64_t capacity, int64_t rows, int heads_q,
@@ -39,7 +40,7 @@ struct KvAttnArgs {
   float *part_lse;         // [splits][rows * heads_q], base 2
   float scale_log2;        // softmax scale * log2(e)
   int32_t window, group, heads_q;
-  int32_t splits, chunk, tiles;
+  int32_t splits, chunk, tiles, join_rows;
   int32_t bf16;            // else binary16
 };
 hipError_t launch_kv_attention(KvAttnArgs a, bool e4m3, const KvAttnPlan &plan, void *ws,

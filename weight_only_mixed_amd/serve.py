@@ -46,9 +46,15 @@ def declare(L):
                              _vp, _vp]
 
 
+_LIB = None
+
+
 def _lib():
-    from . import lib
-    return lib()
+    global _LIB
+    if _LIB is None:
+        from . import lib
+        _LIB = lib()
+    return _LIB
 
 
 def _need(ok: bool, what: str):
@@ -57,13 +63,17 @@ def _need(ok: bool, what: str):
         raise SlqError(SLQ_EINVAL, what)
 
 
-def _run(device, what: str, call):
-    """call(stream) with `device` current; raises on any status but SLQ_OK."""
-    if torch.cuda.current_device() == device.index:
-        status = call(torch.cuda.current_stream(device).cuda_stream)
+_raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle, without a Stream object
+
+
+def _call(device, what: str, fn, *args):
+    """fn(*args, current stream) with `device` current; raises on any status but SLQ_OK."""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            status = call(torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
     if status:
         from . import SlqError
         raise SlqError(status, what)
@@ -130,9 +140,9 @@ class KvSeqs:
 
 
 def _rows(t: torch.Tensor, cache: KvCache, what: str):
-    _need(t.dim() == 3 and t.shape[2] == cache.head_dim and t.dtype in _DTYPE and
-          t.device == cache.device and t.stride(2) == 1,
-          f"{what}: [rows, heads, head_dim], the last dimension contiguous, on the cache's GPU")
+    if not (t.dim() == 3 and t.shape[2] == cache.head_dim and t.dtype in _DTYPE and
+            t.device == cache.device and t.stride(2) == 1):
+        _need(False, f"{what}: [rows, heads, head_dim], the last dimension contiguous, on the cache's GPU")
 
 
 def slq_kv_write(cache: KvCache, seqs: KvSeqs, k: torch.Tensor, v: torch.Tensor,
@@ -145,9 +155,10 @@ def slq_kv_write(cache: KvCache, seqs: KvSeqs, k: torch.Tensor, v: torch.Tensor,
     _need(k.shape == v.shape and k.dtype == v.dtype and k.shape[1] == cache.heads and
           seqs.device == cache.device, "slq_kv_write: k and v of one shape and type, cache heads")
     rows = k.shape[0]
-    _run(cache.device, "slq_kv_write", lambda s: _lib().slq_kv_write(
-        cache._ref, seqs._ref, k.data_ptr(), v.data_ptr(), _DTYPE[k.dtype], rows, k.stride(0),
-        k.stride(1), v.stride(0), v.stride(1), max(1, rows) if max_new is None else max_new, s))
+    ks, vs = k.stride(), v.stride()
+    _call(cache.device, "slq_kv_write", _lib().slq_kv_write, cache._ref, seqs._ref, k.data_ptr(),
+          v.data_ptr(), _DTYPE[k.dtype], rows, ks[0], ks[1], vs[0], vs[1],
+          max(1, rows) if max_new is None else max_new)
 
 
 def slq_kv_read(cache: KvCache, seqs: KvSeqs, rows: int, dtype: torch.dtype = torch.bfloat16,
@@ -164,9 +175,8 @@ def slq_kv_read(cache: KvCache, seqs: KvSeqs, rows: int, dtype: torch.dtype = to
         _need(tuple(t.shape) == shape and t.dtype == dtype and t.device == cache.device and
               t.is_contiguous(), "slq_kv_read: out is contiguous [rows, heads, head_dim] of dtype")
     k, v = out
-    _run(cache.device, "slq_kv_read", lambda s: _lib().slq_kv_read(
-        cache._ref, seqs._ref, k.data_ptr(), v.data_ptr(), _DTYPE[dtype], rows,
-        max(1, rows) if max_rows is None else max_rows, s))
+    _call(cache.device, "slq_kv_read", _lib().slq_kv_read, cache._ref, seqs._ref, k.data_ptr(),
+          v.data_ptr(), _DTYPE[dtype], rows, max(1, rows) if max_rows is None else max_rows)
     return k, v
 
 
@@ -193,10 +203,11 @@ def slq_kv_attention(cache: KvCache, seqs: KvSeqs, q: torch.Tensor, scale: float
     L = _lib()
     nbytes = L.slq_kv_attention_workspace_bytes(cache._ref, seqs._ref, rows, hq, window, mq, ml)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
-    _run(cache.device, "slq_kv_attention", lambda s: L.slq_kv_attention(
-        cache._ref, seqs._ref, q.data_ptr(), _DTYPE[q.dtype], rows, hq, q.stride(0), q.stride(1),
-        1.0 / math.sqrt(dim) if scale is None else scale, window, mq, ml, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), s))
+    qs = q.stride()
+    _call(cache.device, "slq_kv_attention", L.slq_kv_attention, cache._ref, seqs._ref, q.data_ptr(),
+          _DTYPE[q.dtype], rows, hq, qs[0], qs[1], 1.0 / math.sqrt(dim) if scale is None else scale,
+          window, mq, ml, out.data_ptr(), None if lse is None else lse.data_ptr(),
+          None if ws is None else ws.data_ptr())
     return (out, lse) if with_lse else out
 
 
@@ -226,9 +237,9 @@ def slq_sample(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor 
     def ptr(t):
         return None if t is None else t.data_ptr()
 
-    _run(dev, "slq_sample", lambda s: L.slq_sample(
-        logits.data_ptr(), _DTYPE[logits.dtype], rows, vocab, logits.stride(0), ptr(u),
-        ptr(temperature), ptr(top_k), ptr(top_p), ptr(min_p), ptr(tokens), ptr(logprobs), ptr(ws), s))
+    _call(dev, "slq_sample", L.slq_sample, logits.data_ptr(), _DTYPE[logits.dtype], rows, vocab,
+          logits.stride(0), u.data_ptr(), ptr(temperature), ptr(top_k), ptr(top_p), ptr(min_p),
+          tokens.data_ptr(), logprobs.data_ptr(), ptr(ws))
     return tokens, logprobs
 
 
