@@ -93,6 +93,15 @@ __device__ __forceinline__ uint32_t column_pair(uint32_t a, uint32_t b) {
   }
 }
 
+// A load through the scalar cache, of memory that no one writes while the kernel
+// runs and from an address that is the same in every lane: it takes no vector
+// register and does not queue behind the loads of codes.
+template <typename T>
+__device__ __forceinline__ T uniform_load(const T *p) {
+  typedef const __attribute__((address_space(4))) T *Const;
+  return *(Const)(uintptr_t)p;
+}
+
 template <typename F, int... I>
 __device__ __forceinline__ void for_each_int(F &f, std::integer_sequence<int, I...>) {
   (f(std::integral_constant<int, I>()), ...);
@@ -113,19 +122,57 @@ __device__ __forceinline__ uint16_t to_out(float v, bool bf16) {
   return bf16 ? __builtin_bit_cast(uint16_t, (__bf16)v) : __builtin_bit_cast(uint16_t, (_Float16)v);
 }
 
+__device__ __forceinline__ KvSpan uniform_span(const KvAttnArgs &a, int b) {
+  // kv_span on copies of the three entries it reads
+  const int32_t cu[2] = {uniform_load(a.s.cu + b), uniform_load(a.s.cu + b + 1)};
+  const int32_t len = uniform_load(a.s.lens + b);
+  SeqView one = a.s;
+  one.cu = cu;
+  one.lens = &len;
+  return kv_span(one, a.c.shift, 0);
+}
+
+// Tokens per split.  The host knows bounds, not lengths, and a split size that
+// fits the longest sequence leaves the chip half idle on ragged batches (64
+// lengths of 300 .. 8192: 163 us, the compute units busy for 105 of them), so
+// every workgroup sums the lengths itself: an even share of all visible tokens
+// for each of a.share workgroups.  Whole numbers and one division of doubles:
+// the joining kernel comes to the same size.  Every lane returns it.
+__device__ __forceinline__ int split_size(const KvAttnArgs &a) {
+  if (a.share == 0) return a.chunk;
+  double total = 0.0;
+  for (int b = threadIdx.x & (kWave - 1); b < a.s.batch; b += kWave) {
+    const KvSpan sp = kv_span(a.s, a.c.shift, b);
+    if (sp.n > 0) {
+      const KvRange r = kv_visible(sp, a.window, 0, sp.n - 1);
+      total += (double)(r.hi - r.lo);
+    }
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) total += __shfl_xor(total, o, kWave);
+  const double size = ceil(total * (double)(a.c.heads * a.tiles) / (double)a.share);
+  // the same in every lane; said so, or all addresses become per-lane values
+  return __builtin_amdgcn_readfirstlane((int)fmin(fmax(size, (double)a.chunk), 1073741824.0));
+}
+
 // What the workgroups of one (sequence, tile of query rows) share: the token
-// range and how many splits of it hold any token.
+// range, how many splits of it hold any token, and their size.
 struct TileRange {
-  int lo, hi, start, active;
+  int lo, hi, start, active, chunk;
 };
 __device__ __forceinline__ TileRange tile_range(const KvAttnArgs &a, const KvSpan &sp, int rho0,
-                                                int rho1) {
+                                                int rho1, int size) {
   const KvRange r = kv_visible(sp, a.window, rho0 / a.group, (rho1 - 1) / a.group);
   TileRange t;
   t.lo = r.lo;
   t.hi = r.hi;
   t.start = r.lo & ~(kBlock - 1);
-  t.active = r.hi > r.lo ? min((r.hi - t.start + a.chunk - 1) / a.chunk, a.splits) : 0;
+  const int n = r.hi > r.lo ? r.hi - t.start : 0;
+  // as many splits as `size` asks for, within the grid, of equal size
+  const int want = min(max((n - 1) / size + 1, 1), a.splits);
+  t.chunk = ((n - 1) / want + a.grain) / a.grain * a.grain;
+  t.chunk = max(t.chunk, a.grain);
+  t.active = n > 0 ? min((n - 1) / t.chunk + 1, a.splits) : 0;
   return t;
 }
 
@@ -145,9 +192,11 @@ __global__ __launch_bounds__(kThreads, (D <= 128 && NT == 1 ? 4 : 1)) void kv_at
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int col = lane & 15, g = lane >> 4;
-  const int b = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
-  const int h = blockIdx.y;
-  const KvSpan sp = kv_span(a.s, a.c.shift, b);
+  const int slot = a.heads_first ? blockIdx.y : blockIdx.x;
+  const int b = slot / a.splits, split = slot % a.splits;
+  const int h = a.heads_first ? blockIdx.x : blockIdx.y;
+  const int size = split_size(a);
+  const KvSpan sp = uniform_span(a, b);
   const int total = sp.n * a.group;
   const uint8_t *kbase = a.c.codes[0] + (int64_t)h * a.c.head_stride;
   const uint8_t *vbase = a.c.codes[1] + (int64_t)h * a.c.head_stride;
@@ -157,10 +206,10 @@ __global__ __launch_bounds__(kThreads, (D <= 128 && NT == 1 ? 4 : 1)) void kv_at
 
   for (int rho0 = blockIdx.z * ROWS; rho0 < total; rho0 += a.tiles * ROWS) {
     const int rho1 = min(rho0 + ROWS, total);
-    const TileRange tr = tile_range(a, sp, rho0, rho1);
+    const TileRange tr = tile_range(a, sp, rho0, rho1, size);
     if (split >= max(tr.active, a.splits == 1 ? 1 : 0)) continue;   // nothing here (uniform)
-    const int t0 = tr.start + split * a.chunk;
-    const int t1 = split == a.splits - 1 ? tr.hi : min(tr.hi, t0 + a.chunk);
+    const int t0 = tr.start + split * tr.chunk;
+    const int t1 = split == a.splits - 1 ? tr.hi : min(tr.hi, t0 + tr.chunk);
 
     // queries: lane (col, g) holds dims 64 h2 + 16 g + 8 e + t of query col
     u32x4_t qf[NT][KS];
@@ -229,27 +278,25 @@ __global__ __launch_bounds__(kThreads, (D <= 128 && NT == 1 ? 4 : 1)) void kv_at
       u32x4_t kw[2][KL];
       uint32_t vw[2][4][VW];
     };
-    // A tile wholly outside the visible range is not looked at: its page may
-    // belong to someone else by now.  Page numbers are read a step ahead.
-    auto page_ids = [&](int blk, int (&id)[2]) {
+    auto entries = [&](int blk, int (&e)[2]) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int tok = blk + 16 * u;
-        id[u] = tok < t1 && tok < tr.hi && tok + 16 > tr.lo
-                    ? kv_page(a.s, a.c.pages, b, tok >> a.c.shift) : -1;
-      }
+      for (int u = 0; u < 2; ++u)
+        e[u] = uniform_load(a.s.table + kv_entry(a.s, b, (blk + 16 * u) >> a.c.shift));
     };
-    auto load = [&](int blk, const int (&id)[2], Block &x) {
+    auto load = [&](int blk, const int (&e)[2], Block &x) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int tok = blk + 16 * u;
-        x.id[u] = __builtin_amdgcn_readfirstlane(id[u]);
+        // a tile wholly outside the visible range is not looked at: its page may
+        // belong to someone else by now
+        x.id[u] = tok < tr.hi && tok + 16 > tr.lo
+                      ? kv_page_of(a.s, a.c.pages, tok >> a.c.shift, e[u]) : -1;
         x.sk[u] = x.sv[u] = 0.f;
         if (x.id[u] >= 0) {
           const int64_t at = (int64_t)x.id[u] * a.c.page_stride +
                              (int64_t)(tok & ((1 << a.c.shift) - 1)) * a.c.token_stride;
-          x.sk[u] = a.c.scales[0][(int64_t)x.id[u] * a.c.heads + h];
-          x.sv[u] = a.c.scales[1][(int64_t)x.id[u] * a.c.heads + h];
+          x.sk[u] = uniform_load(a.c.scales[0] + (int64_t)x.id[u] * a.c.heads + h);
+          x.sv[u] = uniform_load(a.c.scales[1] + (int64_t)x.id[u] * a.c.heads + h);
           const uint8_t *kp = kbase + at, *vp = vbase + at;
 #pragma unroll
           for (int k = 0; k < KL; ++k) x.kw[u][k] = *reinterpret_cast<const u32x4_t *>(kp + koff + 64 * k);
@@ -373,12 +420,12 @@ __global__ __launch_bounds__(kThreads, (D <= 128 && NT == 1 ? 4 : 1)) void kv_at
     };
     // (a second block in flight per wave costs more occupancy than it hides:
     // 237 us against 188 for 64 sequences of up to 8192 tokens)
-    int id[2];
-    page_ids(t0 + kBlock * wave, id);
+    int e[2];   // table entries, read a step ahead
+    entries(t0 + kBlock * wave, e);
     for (int blk = t0 + kBlock * wave; blk < t1; blk += kBlock * kWaves) {
       Block x;
-      load(blk, id, x);
-      page_ids(blk + kBlock * kWaves, id);
+      load(blk, e, x);
+      entries(blk + kBlock * kWaves, e);
       step(blk, x);
     }
 
@@ -498,7 +545,8 @@ __global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs
   // heads vary fastest over the workgroups: neighbours go to different chiplets,
   // and the tiles of one head's tokens share a chiplet's L2
   const int h = blockIdx.x, b = blockIdx.y / a.splits, split = blockIdx.y % a.splits;
-  const KvSpan sp = kv_span(a.s, a.c.shift, b);
+  const int size = split_size(a);
+  const KvSpan sp = uniform_span(a, b);
   const int total = sp.n * a.group;
   const uint8_t *kbase = a.c.codes[0] + (int64_t)h * a.c.head_stride;
   const uint8_t *vbase = a.c.codes[1] + (int64_t)h * a.c.head_stride;
@@ -521,10 +569,10 @@ __global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs
   const int ntiles = (total + kPromptRows - 1) / kPromptRows;
   for (int tile = ntiles - 1 - (int)blockIdx.z; tile >= 0; tile -= a.tiles) {
     const int rho0 = tile * kPromptRows, rho1 = min(rho0 + kPromptRows, total);
-    const TileRange tr = tile_range(a, sp, rho0, rho1);
+    const TileRange tr = tile_range(a, sp, rho0, rho1, size);
     if (split >= max(tr.active, a.splits == 1 ? 1 : 0)) continue;   // nothing here (uniform)
-    const int t0 = tr.start + split * a.chunk;
-    const int t1 = split == a.splits - 1 ? tr.hi : min(tr.hi, t0 + a.chunk);
+    const int t0 = tr.start + split * tr.chunk;
+    const int t1 = split == a.splits - 1 ? tr.hi : min(tr.hi, t0 + tr.chunk);
 
     // queries: lane (col, half) holds dims 16 k + 8 half + t of query col
     const int rho = rho0 + 32 * wave + col;
@@ -585,11 +633,13 @@ __global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs
     u32x4_t kreg;
     uint32_t vreg[4];
     float skreg, svreg;
-    auto page_id = [&](int base) {
-      const int tok = (base + wtok) & ~15;   // the group's first: its waves agree
-      return tok < t1 && tok + 16 > tr.lo ? kv_page(a.s, a.c.pages, b, tok >> a.c.shift) : -1;
+    auto entry = [&](int base) {
+      return uniform_load(a.s.table + kv_entry(a.s, b, (base + wtok) >> a.c.shift));
     };
-    auto load = [&](int base, int id) {
+    auto load = [&](int base, int e) {
+      const int tok = (base + wtok) & ~15;   // the group's first: its waves agree
+      const int id = tok < t1 && tok + 16 > tr.lo
+                         ? kv_page_of(a.s, a.c.pages, tok >> a.c.shift, e) : -1;
       kreg = u32x4_t{0, 0, 0, 0};
       vreg[0] = vreg[1] = vreg[2] = vreg[3] = 0u;
       skreg = -1.f;
@@ -602,8 +652,8 @@ __global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs
 #pragma unroll
         for (int t = 0; t < 4; ++t, vp += a.c.token_stride)
           vreg[t] = *reinterpret_cast<const uint32_t *>(vp + voff);
-        skreg = a.c.scales[0][(int64_t)id * a.c.heads + h];
-        svreg = a.c.scales[1][(int64_t)id * a.c.heads + h];
+        skreg = uniform_load(a.c.scales[0] + (int64_t)id * a.c.heads + h);
+        svreg = uniform_load(a.c.scales[1] + (int64_t)id * a.c.heads + h);
       }
     };
     auto store = [&](int base, int buf) {
@@ -633,16 +683,16 @@ __global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs
       }
     };
 
-    int id = page_id(t0), id_next = page_id(t0 + TOK);
+    int e_next = entry(t0 + TOK);   // table entries, read a tile ahead
     __syncthreads();   // the previous tile's last readers
-    load(t0, id);
+    load(t0, entry(t0));
     store(t0, 0);
     __syncthreads();
     for (int base = t0, buf = 0; base < t1; base += TOK, buf ^= 1) {
       const bool more = base + TOK < t1;
       if (more) {
-        load(base + TOK, id_next);
-        id_next = page_id(base + 2 * TOK);
+        load(base + TOK, e_next);
+        e_next = entry(base + 2 * TOK);
       }
       if (wave_on && base < any_hi && base + TOK > any_lo) {
         float f[GR], sv[GR];
@@ -792,12 +842,13 @@ __global__ __launch_bounds__(kThreads) void kv_attn_join_kernel(KvAttnArgs a, in
   __shared__ float m_lds[kWaves], l_lds[kWaves];
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int b = blockIdx.x, h = blockIdx.y;
-  const KvSpan sp = kv_span(a.s, a.c.shift, b);
+  const int size = split_size(a);
+  const KvSpan sp = uniform_span(a, b);
   const int total = sp.n * a.group;
   const int64_t step = (int64_t)a.s.rows * a.heads_q;
   for (int rho = blockIdx.z; rho < total; rho += gridDim.z) {
     const int rho0 = rho / tile_rows * tile_rows;
-    const TileRange tr = tile_range(a, sp, rho0, min(rho0 + tile_rows, total));
+    const TileRange tr = tile_range(a, sp, rho0, min(rho0 + tile_rows, total), size);
     const int i = rho / a.group, hd = rho % a.group;
     const int64_t row = (int64_t)(sp.row0 + i) * a.heads_q + h * a.group + hd;
     float m = -INFINITY, l = 0.f, o[PER] = {};
@@ -859,7 +910,8 @@ __global__ __launch_bounds__(kThreads) void kv_attn_join_kernel(KvAttnArgs a, in
 
 template <int D, int NT>
 void launch_decode(const KvAttnArgs &a, bool e4m3, hipStream_t st) {
-  const dim3 grid((unsigned)a.s.batch * (unsigned)a.splits, (unsigned)a.c.heads, (unsigned)a.tiles);
+  const unsigned slots = (unsigned)a.s.batch * (unsigned)a.splits, heads = (unsigned)a.c.heads;
+  const dim3 grid(a.heads_first ? heads : slots, a.heads_first ? slots : heads, (unsigned)a.tiles);
   if (e4m3)
     hipLaunchKernelGGL((kv_attn_kernel<D, true, NT>), grid, dim3(kThreads), 0, st, a);
   else
@@ -907,13 +959,20 @@ KvAttnPlan kv_attn_plan(int batch, int heads, int dim, int64_t capacity, int64_t
   if (window > 0) span = std::min<int64_t>(span, (int64_t)window + tile_rows / group + 1);
   span += kBlock - 1;   // a range may start up to 31 tokens before its first visible one
   const int64_t base = (int64_t)batch * heads * p.tiles;
-  const int64_t kStep = p.nt == 0 ? 8192 / dim : kBlock * kWaves;   // one step of every wave
-  const int64_t kTarget = p.nt == 0 ? 512 : 2048;   // workgroups that fill the chip
-  int64_t splits = std::max<int64_t>(1, std::min<int64_t>(kTarget / base, (span + kStep - 1) / kStep));
-  splits = std::min<int64_t>(splits, 256);
-  const int64_t chunk = ((span + splits - 1) / splits + kStep - 1) / kStep * kStep;
-  p.splits = (int)((span + chunk - 1) / chunk);
-  p.chunk = (int)chunk;
+  // one step of every wave
+  p.grain = p.nt == 0 ? 8192 / dim : kBlock * kWaves;
+  // Workgroups to aim for: one per compute unit for the prompt kernel, two
+  // rounds of those that run at once for the decode kernel (64 sequences of 300
+  // .. 8192 tokens: 185 us with one round, 164 with two, 169 with four).
+  const int64_t slots = p.nt == 0 ? 256 : p.nt == 1 && dim <= 128 ? 2048 : 1024;
+  // Splits per sequence: room for one that is four times the mean; more
+  // workgroups than slots need no splitting.  Each sequence's last split is
+  // half full on average, hence the share.
+  int64_t splits = std::min<int64_t>((4 * slots + base - 1) / base, (span + p.grain - 1) / p.grain);
+  if (base >= (p.nt == 0 ? slots : 2 * slots)) splits = 1;
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(splits, 256));
+  p.share = p.splits > 1 ? (int)std::max<int64_t>(slots - base / 2, slots / 2) : 0;
+  p.chunk = p.splits > 1 ? p.grain : 1 << 30;
   if (p.splits > 1)
     p.ws_bytes = (size_t)p.splits * (size_t)rows * (size_t)heads_q * (size_t)(dim + 1) * sizeof(float);
   return p;
@@ -923,6 +982,12 @@ hipError_t launch_kv_attention(KvAttnArgs a, bool e4m3, const KvAttnPlan &plan, 
                                hipStream_t st) {
   a.splits = plan.splits;
   a.chunk = plan.chunk;
+  a.grain = plan.grain;
+  a.share = plan.share;
+  // Pages that keep a head's tokens together: neighbouring workgroups take the
+  // heads of one page (168 us against 175); pages that keep a token's heads
+  // together: neighbours take tokens (129 us against 145).
+  a.heads_first = a.c.head_stride >= a.c.token_stride && (int64_t)a.s.batch * a.splits <= 65535;
   a.tiles = plan.tiles;
   a.join_rows = plan.rows;
   a.part_o = static_cast<float *>(ws);

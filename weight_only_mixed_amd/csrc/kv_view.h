@@ -49,11 +49,16 @@ SLQ_HD KvSpan kv_span(const SeqView &s, int32_t shift, int32_t b) {
   return r;
 }
 
-// The page that holds tokens p << shift .., or -1.
+// The table entry to read for tokens p << shift .. (any p: always inside the
+// table), and the page that the entry read there stands for, or -1.
+SLQ_HD int64_t kv_entry(const SeqView &s, int32_t b, int32_t p) {
+  return (int64_t)b * s.table_stride + kv_clamp(p, 0, s.max_pages - 1);
+}
+SLQ_HD int32_t kv_page_of(const SeqView &s, int64_t pages, int32_t p, int32_t entry) {
+  return p >= 0 && p < s.max_pages && entry >= 0 && entry < pages ? entry : -1;
+}
 SLQ_HD int32_t kv_page(const SeqView &s, int64_t pages, int32_t b, int32_t p) {
-  if (p < 0 || p >= s.max_pages) return -1;
-  const int32_t id = s.table[(int64_t)b * s.table_stride + p];
-  return id >= 0 && id < pages ? id : -1;
+  return kv_page_of(s, pages, p, s.table[kv_entry(s, b, p)]);
 }
 
 // The new slots [lo, hi) of page p of a sequence (empty: lo >= hi), and the

@@ -22,8 +22,10 @@ hipError_t launch_kv_read(const KvView &c, const SeqView &s, bool e4m3, void *k,
 struct KvAttnPlan {
   int nt;         // 16-query tiles per workgroup of the decode kernel; 0: prompt kernel
   int tiles;      // workgroups along a sequence's query rows
-  int splits;     // workgroups along the tokens
-  int chunk;      // tokens per split (the last split takes the rest)
+  int splits;     // workgroups along the tokens, at most
+  int chunk;      // tokens per split, at least
+  int grain;      // tokens that splits are multiples of
+  int share;      // workgroups that share all tokens evenly (0: not split)
   int rows;       // query rows per kv head and sequence, as expected
   size_t ws_bytes;
 };
@@ -40,7 +42,8 @@ struct KvAttnArgs {
   float *part_lse;         // [splits][rows * heads_q], base 2
   float scale_log2;        // softmax scale * log2(e)
   int32_t window, group, heads_q;
-  int32_t splits, chunk, tiles, join_rows;
+  int32_t splits, chunk, grain, share, tiles, join_rows;
+  int32_t heads_first;     // grid order of the decode kernel
   int32_t bf16;            // else binary16
 };
 hipError_t launch_kv_attention(KvAttnArgs a, bool e4m3, const KvAttnPlan &plan, void *ws,
