@@ -1,8 +1,8 @@
 // Next-token choice: temperature, top-k, top-p, min-p, from given uniform
 // numbers (semantics in slq_serve.h).
 //
-// Weights w = exp((l - max) / T) are fp64, then whole numbers floor(w * 2^S)
-// with S = 62 - ceil(log2 vocab): sums of them are exact, so histograms may be
+// Weights w = exp((l - max) / T) are fp64, then whole numbers, w * 2^S rounded,
+// with S = min(50, 62 - ceil(log2 vocab)): sums of them are exact, so histograms may be
 // filled with atomics and partial sums taken in any order without changing a
 // result, and a cut falls where the 64-bit definition puts it.
 //
@@ -109,49 +109,49 @@ struct Row {
   typedef typename Logit<T>::Vec Vec;
   const char *base;   // the boundary
   int skip;           // slots before element 0
-  int64_t end;        // slot behind the last element
+  int end;            // slot behind the last element (vocab <= 2^24)
   __device__ __forceinline__ Row(const SampleArgs &a, int64_t r) {
     const char *p = static_cast<const char *>(a.logits) + r * a.row_stride * Logit<T>::kBytes;
     skip = (int)((uintptr_t)p & 15) / Logit<T>::kBytes;
     base = p - skip * Logit<T>::kBytes;
-    end = a.vocab + skip;
+    end = (int)a.vocab + skip;
   }
-  __device__ __forceinline__ float at(int64_t slot) const {
-    return slot >= skip && slot < end ? tame(Logit<T>::one(base + slot * Logit<T>::kBytes)) : -INFINITY;
+  __device__ __forceinline__ float at(int slot) const {
+    return slot >= skip && slot < end ? tame(Logit<T>::one(base + (uint32_t)(slot * Logit<T>::kBytes))) : -INFINITY;
   }
   // whether slots [lo, hi) are all elements of the row
-  __device__ __forceinline__ bool inside(int64_t lo, int64_t hi) const { return lo >= skip && hi <= end; }
+  __device__ __forceinline__ bool inside(int lo, int hi) const { return lo >= skip && hi <= end; }
   // kPer slots from `slot`, a multiple of kPer, wholly inside the row: one load,
   // nothing done with it yet
-  __device__ __forceinline__ Vec raw(int64_t slot) const {
-    return *reinterpret_cast<const Vec *>(base + slot * Logit<T>::kBytes);
+  __device__ __forceinline__ Vec raw(int slot) const {
+    return *reinterpret_cast<const Vec *>(base + (uint32_t)(slot * Logit<T>::kBytes));
   }
   // the same anywhere
-  __device__ __forceinline__ Vec any(int64_t slot) const {
+  __device__ __forceinline__ Vec any(int slot) const {
     if (inside(slot, slot + Logit<T>::kPer)) return raw(slot);
     Vec w;
 #pragma unroll
     for (int i = 0; i < Logit<T>::kPer; ++i)
       Logit<T>::set(w, i, slot + i >= skip && slot + i < end
-                              ? Logit<T>::bits(base + (slot + i) * Logit<T>::kBytes)
+                              ? Logit<T>::bits(base + (uint32_t)((slot + i) * Logit<T>::kBytes))
                               : Logit<T>::kNegInf);
     return w;
   }
-  __device__ __forceinline__ void load(int64_t slot, float *v) const {
+  __device__ __forceinline__ void load(int slot, float *v) const {
     const Vec w = any(slot);
 #pragma unroll
     for (int i = 0; i < Logit<T>::kPer; ++i) v[i] = tame(Logit<T>::get(w, i));
   }
-  // f(v, slot) for the kPer elements of each vector of slots first, first +
-  // step, ... below `stop` (<= end); kU loads in flight
+  // f(v, slot) for the elements of the vectors at slots first, first + step, ..
+  // below `stop`, which ends at a vector's end or the row's (slots behind the
+  // row read as -inf); kU loads in flight
   template <int kU, typename F>
-  __device__ __forceinline__ void each(int64_t first, int64_t step, int64_t stop, F &&f) const {
+  __device__ __forceinline__ void each(int first, int step, int stop, F &&f) const {
     constexpr int P = Logit<T>::kPer;
-    for (int64_t s = first; s < stop; s += kU * step) {
+    for (int s = first; s < stop; s += kU * step) {
       Vec w[kU];
       // one branch for all: a load inside a divergent branch waits there
-      const bool in = __all(inside(s, s + (kU - 1) * step + P));
-      if (in) {
+      if (__all(inside(s, s + (kU - 1) * step + P))) {
 #pragma unroll
         for (int u = 0; u < kU; ++u) w[u] = raw(s + u * step);
       } else {
@@ -160,9 +160,9 @@ struct Row {
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u)
+        if (s + u * step < stop)
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-          if (s + u * step + i < stop) f(tame(Logit<T>::get(w[u], i)), s + u * step + i);
+          for (int i = 0; i < P; ++i) f(tame(Logit<T>::get(w[u], i)), s + u * step + i);
     }
   }
 };
@@ -180,34 +180,40 @@ __device__ __forceinline__ float value_of(uint32_t k) {
 // key after that of -0, which no logit has.
 __device__ __forceinline__ float limit_of(uint32_t k) { return value_of(k == 0x7FFFFFFFu ? k - 1 : k); }
 
-// exp(x) for x <= 0 in fp64: x = n ln 2 + f, |f| <= ln 2 / 2, Taylor series of
-// degree 12 (remainder below 2e-16).  Below 2^-64 it is 0.
-__device__ __forceinline__ double exp_neg(double x) {
-  const double n = rint(x * 1.4426950408889634);
+// 2^y for y <= 0 in fp64: y = n + f, |f| <= 1/2, and the series of 2^f =
+// exp(f ln 2) to degree 11 (coefficients ln(2)^k / k!, remainder below 1e-14).
+// Below 2^-64 it is 0.
+__device__ __forceinline__ double exp2_neg(double y) {
+  const double n = rint(y);
   if (!(n > -64.0)) return 0.0;
-  const double f = fma(n, -2.3190468138462996e-17, fma(n, -0.6931471805599453, x));
-  double r = 1.0 / 479001600;
-  r = fma(r, f, 1.0 / 39916800);
-  r = fma(r, f, 1.0 / 3628800);
-  r = fma(r, f, 1.0 / 362880);
-  r = fma(r, f, 1.0 / 40320);
-  r = fma(r, f, 1.0 / 5040);
-  r = fma(r, f, 1.0 / 720);
-  r = fma(r, f, 1.0 / 120);
-  r = fma(r, f, 1.0 / 24);
-  r = fma(r, f, 1.0 / 6);
-  r = fma(r, f, 0.5);
-  r = fma(r, f, 1.0);
+  const double f = y - n;
+  double r = 4.44553827187081e-10;
+  r = fma(r, f, 7.054911620801121e-09);
+  r = fma(r, f, 1.0178086009239696e-07);
+  r = fma(r, f, 1.3215486790144305e-06);
+  r = fma(r, f, 1.5252733804059838e-05);
+  r = fma(r, f, 0.00015403530393381606);
+  r = fma(r, f, 0.0013333558146428441);
+  r = fma(r, f, 0.009618129107628477);
+  r = fma(r, f, 0.055504108664821576);
+  r = fma(r, f, 0.2402265069591007);
+  r = fma(r, f, 0.6931471805599453);
   r = fma(r, f, 1.0);
   return ldexp(r, (int)n);
 }
 
+constexpr double kLog2e = 1.4426950408889634;
+
+// w = exp((l - max) / T) and its mass, w * 2^S to the nearest whole number.
+// S <= 50, so the mass is what adding 2^52 leaves in the low bits of a double.
 struct Weigh {
-  double max, inv_t, unit;
+  double max, inv_t, scale, unit;   // scale = log2(e) / T, unit = 2^S
   __device__ __forceinline__ double weight(float v) const {
-    return v == -INFINITY ? 0.0 : exp_neg(((double)v - max) * inv_t);
+    return v == -INFINITY ? 0.0 : exp2_neg(((double)v - max) * scale);
   }
-  __device__ __forceinline__ uint64_t mass(double w) const { return (uint64_t)(w * unit); }
+  __device__ __forceinline__ uint64_t mass(double w) const {
+    return __builtin_bit_cast(uint64_t, fma(w, unit, 0x1p52)) & 0xFFFFFFFFFFFFFull;
+  }
 };
 
 __device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
@@ -281,7 +287,7 @@ __global__ __launch_bounds__(kUnitThreads, 4) void sample_units_kernel(SampleArg
     const Row<T> row(a, r);
     const Cuts cuts(a, r);
     const bool with_mass = cuts.row_mass(a.vocab);
-    const double inv_t = with_mass ? 1.0 / (double)cuts.temp : 0.0;
+    const double scale = with_mass ? 1.0 / (double)cuts.temp * kLog2e : 0.0;
     const int beg = unit * steps * kBatch;   // slots fit an int: vocab <= 2^24
     uint32_t bound = kKeyNegInf;
     float limit = -INFINITY;                 // v > limit: key above the bound
@@ -322,14 +328,14 @@ __global__ __launch_bounds__(kUnitThreads, 4) void sample_units_kernel(SampleArg
       if (with_mass) {
         const float t = wave_max(mx);
         if (t > top) {
-          if (top != -INFINITY) mass *= exp_neg(((double)top - (double)t) * inv_t);
+          if (top != -INFINITY) mass *= exp2_neg(((double)top - (double)t) * scale);
           top = t;
         }
         if (top != -INFINITY) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float x = tame(v[e]);
-            mass += x == -INFINITY ? 0.0 : exp_neg(((double)x - (double)top) * inv_t);
+            mass += x == -INFINITY ? 0.0 : exp2_neg(((double)x - (double)top) * scale);
           }
         }
       }
@@ -480,7 +486,7 @@ __device__ Cut descend(const Row<T> &row, const Weigh &wg, bool by_mass, bool wi
       sh.hist.mass[i] = 0;
     }
     __syncthreads();
-    row.template each<4>((int64_t)threadIdx.x * P, kThreads * P, row.end, [&](float v, int64_t) {
+    row.template each<16 / P>((int)threadIdx.x * P, kThreads * P, row.end, [&](float v, int) {
       const uint32_t k = key_of(v);
       if (k > kKeyNegInf && (level == 0 || k >> shift == prefix)) {
         const uint32_t d = (k >> next) & (bins - 1);
@@ -568,7 +574,7 @@ __device__ Prefix row_prefix(const Row<T> &row, const Weigh &wg, bool by_mass, b
     sh.digit = kBins;
   }
   __syncthreads();
-  row.template each<4>((int64_t)threadIdx.x * P, kThreads * P, row.end, [&](float v, int64_t) {
+  row.template each<16 / P>((int)threadIdx.x * P, kThreads * P, row.end, [&](float v, int) {
     if (v == -INFINITY) return;
     const int d = bin_of(v);
     if (!by_mass) atomicAdd(&sh.hist.count[d], 1u);
@@ -596,7 +602,7 @@ __device__ Prefix row_prefix(const Row<T> &row, const Weigh &wg, bool by_mass, b
   const int bin = (int)sh.digit;
   const uint64_t above_n = sh.above_n, above_m = sh.above_m;
   if (bin < kBins - 1) {
-    row.template each<4>((int64_t)threadIdx.x * P, kThreads * P, row.end, [&](float v, int64_t slot) {
+    row.template each<16 / P>((int)threadIdx.x * P, kThreads * P, row.end, [&](float v, int slot) {
       if (v == -INFINITY || bin_of(v) != bin) return;
       const uint32_t at = atomicAdd(&sh.listed, 1u);
       if (at < kList)
@@ -666,7 +672,7 @@ __device__ Prefix row_prefix(const Row<T> &row, const Weigh &wg, bool by_mass, b
 // taken of (0: the mass found).
 template <int T>
 __device__ void draw(const SampleArgs &a, int64_t r, const Row<T> &row, const Weigh &wg,
-                     uint32_t tau, uint64_t quota, double min_w, int64_t beg, int64_t end,
+                     uint32_t tau, uint64_t quota, double min_w, int beg, int end,
                      double target, double total, Shared &sh) {
   constexpr int P = Logit<T>::kPer;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
@@ -683,16 +689,16 @@ __device__ void draw(const SampleArgs &a, int64_t r, const Row<T> &row, const We
     }
   };
   do {
-    const int64_t len = end - beg;
+    const int len = end - beg;
     const bool wide = len > kWave * kWaves;   // whole vectors per lane
-    const int64_t grain = wide ? kWave * P : kWave;
-    const int64_t seg = ((len + kWaves - 1) / kWaves + grain - 1) / grain * grain;
-    const int64_t s0 = min(beg + seg * wave, end), s1 = min(s0 + seg, end);
+    const int grain = wide ? kWave * P : kWave;
+    const int seg = ((len + kWaves - 1) / kWaves + grain - 1) / grain * grain;
+    const int s0 = min(beg + seg * wave, end), s1 = min(s0 + seg, end);
     uint64_t m = 0, t = 0;
     if (wide) {
-      row.template each<4>(s0 + lane * P, kWave * P, s1, [&](float v, int64_t) { take(v, m, t); });
+      row.template each<16 / P>(s0 + lane * P, kWave * P, s1, [&](float v, int) { take(v, m, t); });
     } else {
-      for (int64_t s = s0 + lane; s < s1; s += kWave) take(row.at(s), m, t);
+      for (int s = s0 + lane; s < s1; s += kWave) take(row.at(s), m, t);
     }
     m = wave_sum_u64(m);
     t = wave_sum_u64(t);
@@ -735,12 +741,12 @@ __device__ void draw(const SampleArgs &a, int64_t r, const Row<T> &row, const We
     }
     ties_before = pick < 0 ? last_tb : tb;
     mass_before = pick < 0 ? last_mb : mb;
-    const int64_t n0 = min(beg + seg * (pick < 0 ? last : pick), end);
+    const int n0 = min(beg + seg * (pick < 0 ? last : pick), end);
     end = min(n0 + seg, end);
     beg = n0;
   } while (end - beg > kWave);
   if (wave == 0) {
-    const int64_t slot = beg + lane;
+    const int slot = beg + lane;
     const float v = slot < end ? row.at(slot) : -INFINITY;
     uint64_t m = 0, t = 0;
     if (slot < end) take(v, m, t);
@@ -905,7 +911,7 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, con
   }
   __syncthreads();
   if (per_row == 0) {
-    for (int64_t s = (int64_t)threadIdx.x * P; s < row.end; s += kThreads * P) {
+    for (int s = threadIdx.x * P; s < row.end; s += kThreads * P) {
       float v[P];
       row.load(s, v);
 #pragma unroll
@@ -935,9 +941,9 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, con
       for (int i = threadIdx.x; i < per_row; i += kThreads)
         if (units[i].top == top) first = max(first, (uint64_t)(uint32_t)~(uint32_t)i);
       const int unit = (int)~(uint32_t)block_max_u64(first, sh);
-      const int64_t s0 = (int64_t)unit * unit_slots, s1 = min(s0 + unit_slots, row.end);
+      const int s0 = unit * unit_slots, s1 = min(s0 + unit_slots, row.end);
       best = 0;
-      for (int64_t s = s0 + threadIdx.x; s < s1; s += kThreads)
+      for (int s = s0 + threadIdx.x; s < s1; s += kThreads)
         if (row.at(s) == top) best = max(best, (uint64_t)(uint32_t)~(uint32_t)(s - row.skip));
       best = block_max_u64(best, sh);
     }
@@ -947,8 +953,9 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, con
     }
     return;
   }
-  const int s = 62 - (a.vocab > 1 ? 64 - __builtin_clzll((uint64_t)a.vocab - 1) : 0);
-  const Weigh wg{(double)top, 1.0 / (double)cuts.temp, ldexp(1.0, s)};
+  const int s = min(50, 62 - (a.vocab > 1 ? 64 - __builtin_clzll((uint64_t)a.vocab - 1) : 0));
+  const double inv_t = 1.0 / (double)cuts.temp;
+  const Weigh wg{(double)top, inv_t, inv_t * kLog2e, ldexp(1.0, s)};
 
   // the row's mass, in the order of the units
   double row_mass = 0.0;
@@ -967,10 +974,13 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, con
     row_mass *= wg.unit;
   }
 
+  // what the draw at the end takes: by default the whole row
+  int beg = 0, end = row.end;
+  double target = -1.0, total = 0.0;
   if (per_row > 0 && free_draw) {
     // the unit that holds the draw: wave 0 scans the units' masses by index
     const float u = a.u[r];
-    const double target = fmin((double)(u > 0.f ? u : 0.f), 1.0 - 0x1p-53) * row_mass;
+    target = fmin((double)(u > 0.f ? u : 0.f), 1.0 - 0x1p-53) * row_mass;
     __syncthreads();
     if (wave == 0) {
       double before = 0.0;
@@ -1007,16 +1017,15 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, con
       }
     }
     __syncthreads();
-    const int64_t at = sh.pos;
-    const double rest = target - sh.d[0];
+    beg = (int)sh.pos * unit_slots;
+    end = min(beg + unit_slots, row.end);
+    target = fmax(target - sh.d[0], 0.0);
+    total = row_mass;
     __syncthreads();
-    draw<T>(a, r, row, wg, 0u, 0, 0.0, at * unit_slots, min((at + 1) * unit_slots, row.end),
-            rest > 0.0 ? rest : 0.0, row_mass, sh);
-    return;
   }
 
   // the listed elements above the bound
-  if (per_row > 0) {
+  if (per_row > 0 && !free_draw) {
     // a wave takes units wave, wave + 16, ..; lists are read whole (entries
     // behind a unit's count are whatever the workspace held) so that count and
     // entries are one round trip
@@ -1052,7 +1061,7 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, con
   const int64_t n_k = min<int64_t>(cuts.k, listed);
   const int i0 = 2 * threadIdx.x;
   // whether the kept set is known to end inside the list
-  bool inside = listed > 0 && listed <= kList;
+  bool inside = listed > 0 && listed <= kList && (per_row == 0 || !free_draw);
   if (inside && (listed > kPairs || !k_inside)) {
     // Narrow the list to a shorter prefix that still holds the kept set, by a
     // histogram of its keys: through the n_k-th element, or the nucleus; and
@@ -1160,28 +1169,27 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, con
     return;
   }
 
-  // the kept set ends outside the list
+  // the kept set ends outside the list (or is the whole row)
   uint32_t tau = 0;                 // kept: key > tau, or == tau and among the first `quota` ties
   uint64_t quota = 0;
   double of_mass = row_mass;
-  if (cuts.k < a.vocab) {
-    const Prefix c = row_prefix<T>(row, wg, false, cuts.p < 1.0, (uint64_t)cuts.k, 0.0, sh);
-    tau = c.tau;
-    quota = c.quota;
-    of_mass = (double)c.mass;
-  }
-  if (cuts.p < 1.0) {
-    // shortest prefix with mass >= p * of_mass; at least one token
-    const Prefix c = row_prefix<T>(row, wg, true, true, 0, fmax(cuts.p * of_mass, 1.0), sh);
+#pragma unroll 1
+  for (int cut = 0; cut < 2; ++cut) {   // top_k, then top_p (one copy of the code)
+    const bool by_mass = cut == 1;
+    if (by_mass ? !(cuts.p < 1.0) : cuts.k == a.vocab) continue;
+    // the shortest prefix with mass >= p * of_mass has at least one token
+    const Prefix c = row_prefix<T>(row, wg, by_mass, by_mass || cuts.p < 1.0, (uint64_t)cuts.k,
+                                   fmax(cuts.p * of_mass, 1.0), sh);
     if (c.tau > tau) {
       tau = c.tau;
       quota = c.quota;
     } else if (c.tau == tau && c.quota < quota) {
       quota = c.quota;
     }
+    of_mass = (double)c.mass;
   }
   __syncthreads();
-  draw<T>(a, r, row, wg, tau, quota, cuts.min_w, 0, row.end, -1.0, 0.0, sh);
+  draw<T>(a, r, row, wg, tau, quota, cuts.min_w, beg, end, target, total, sh);
 }
 
 struct SamplePlan {
