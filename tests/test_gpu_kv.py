@@ -171,6 +171,28 @@ def test_unusual_values(fmt):
 
 
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_codes_are_of_rounded_quotients(fmt):
+    """Many mantissas at many scales, and values within an ulp of the border between
+    two codes: the quotient is the IEEE one whichever way it is computed."""
+    g = np.random.default_rng(21)
+    pages, page = 200, 256
+    box = Box(pages, 1, 256, page, fmt)
+    x = g.standard_normal((pages, page, 256)) * 2.0 ** g.uniform(-70, 70, (pages, 1, 1))
+    x = x.astype(np.float32)
+    for p in range(pages):
+        s = np.abs(x[p]).max() * (np.float32(1) / np.float32(127 if fmt == "int8" else 448))
+        edge = (g.integers(-126, 126, 30000) + 0.5).astype(np.float32) * s
+        at = 1 + g.permutation(page * 256 - 1)[:30000]
+        flat = x[p].reshape(-1)
+        top = np.abs(flat).argmax()
+        near = edge * (1 + np.float32(2.0 ** -23) * g.integers(-1, 2, 30000).astype(np.float32))
+        flat[at[at != top]] = near[at != top]
+    x = torch.from_numpy(x.reshape(pages * page, 1, 256)).to(DEV)
+    box.write(np.arange(pages)[None], np.array([pages * page]), np.array([0, pages * page]), x, -x)
+    box.same()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 def test_positions_and_pages_that_do_not_exist(fmt):
     """Negative positions, pages out of range, lengths behind the table, offsets
     behind the rows: not written, read as 0, the rest as usual."""

@@ -43,9 +43,9 @@ def read(c=None, s=None, k=P[7], v=P[8], dtype=1, rows=4, max_rows=4):
     return slq.lib().slq_kv_read(ctypes.addressof(c), ctypes.addressof(s), k, v, dtype, rows, max_rows, None)
 
 
-def attn(c=None, s=None, q=P[7], dtype=1, rows=4, hq=32, st=(4096, 128), scale=0.1, window=0, mq=1, ml=640,
+def attn(c=None, s=None, q=P[7], dtype=1, rows=4, hq=32, st=(4096, 128), scale=0.1, window=0, mq=1, ml=100000,
          out=P[8], lse=P[9], ws=P[10]):
-    c, s = c or cache(), s or seqs()
+    c, s = c or cache(), s or seqs(width=2000)     # long enough to be split: a workspace is needed
     return slq.lib().slq_kv_attention(ctypes.addressof(c), ctypes.addressof(s), q, dtype, rows, hq, *st, scale,
                                       window, mq, ml, out, lse, ws, None)
 

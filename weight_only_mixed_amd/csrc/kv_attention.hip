@@ -45,6 +45,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kBlock = 32;            // tokens per wave and step
+constexpr int kWideSpan = 1280;       // tokens that 8 waves take in one piece
 constexpr float kPUnit = 2048.f;      // probabilities are held times this
 constexpr float kSlack = 4.f;         // and may reach 2^kSlack
 constexpr float kLn2 = 0.6931471805599453f;
@@ -178,16 +179,17 @@ __device__ __forceinline__ TileRange tile_range(const KvAttnArgs &a, const KvSpa
 
 // Four waves per SIMD for single tokens: what hides the loads is waves, not
 // blocks in flight per wave.
-template <int D, bool E4M3, int NT>
-__global__ __launch_bounds__(kThreads, (D <= 128 && NT == 1 ? 4 : 1)) void kv_attn_kernel(KvAttnArgs a) {
+// W waves share a workgroup's tokens: 4, or 8 for a short sequence in one piece.
+template <int D, bool E4M3, int NT, int W>
+__global__ __launch_bounds__(W *kWave, (D <= 128 && NT == 1 && W == 4 ? 4 : 1)) void kv_attn_kernel(KvAttnArgs a) {
   constexpr int KS = D / 32;      // MFMA k steps of q . k
   constexpr int VJ = D / 16;      // bytes of a V row per lane, and MFMAs of p . v
   constexpr int KL = D / 64;      // 16-byte K loads per token and lane
   constexpr int VW = VJ / 4;      // 32-bit words of a V row per lane
   constexpr int ROWS = 16 * NT;
   constexpr int OP = D + 4;       // pitch of a query's outputs in LDS
-  __shared__ float o_lds[kWaves][16 * OP];
-  __shared__ float m_lds[kWaves][16], l_lds[kWaves][16];
+  __shared__ float o_lds[W][16 * OP];
+  __shared__ float m_lds[W][16], l_lds[W][16];
 
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -422,10 +424,10 @@ __global__ __launch_bounds__(kThreads, (D <= 128 && NT == 1 ? 4 : 1)) void kv_at
     // 237 us against 188 for 64 sequences of up to 8192 tokens)
     int e[2];   // table entries, read a step ahead
     entries(t0 + kBlock * wave, e);
-    for (int blk = t0 + kBlock * wave; blk < t1; blk += kBlock * kWaves) {
+    for (int blk = t0 + kBlock * wave; blk < t1; blk += kBlock * W) {
       Block x;
       load(blk, e, x);
-      entries(blk + kBlock * kWaves, e);
+      entries(blk + kBlock * W, e);
       step(blk, x);
     }
 
@@ -448,13 +450,13 @@ __global__ __launch_bounds__(kThreads, (D <= 128 && NT == 1 ? 4 : 1)) void kv_at
       __syncthreads();
       const int qc = threadIdx.x / 16, d0 = (threadIdx.x % 16) * VJ;
       const int rho = rho0 + 16 * n + qc;
-      if (rho < rho1) {
+      if (threadIdx.x < 256 && rho < rho1) {
         float mt = m_lds[0][qc];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) mt = fmaxf(mt, m_lds[w][qc]);
+        for (int w = 1; w < W; ++w) mt = fmaxf(mt, m_lds[w][qc]);
         float lsum = 0.f, o[VJ] = {};
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
+        for (int w = 0; w < W; ++w) {
           const float f2 = l_lds[w][qc] > 0.f ? exp2_hw(m_lds[w][qc] - mt) : l_lds[w][qc];
           lsum += f2 * l_lds[w][qc];
 #pragma unroll
@@ -908,14 +910,14 @@ __global__ __launch_bounds__(kThreads) void kv_attn_join_kernel(KvAttnArgs a, in
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, int W = kWaves>
 void launch_decode(const KvAttnArgs &a, bool e4m3, hipStream_t st) {
   const unsigned slots = (unsigned)a.s.batch * (unsigned)a.splits, heads = (unsigned)a.c.heads;
   const dim3 grid(a.heads_first ? heads : slots, a.heads_first ? slots : heads, (unsigned)a.tiles);
   if (e4m3)
-    hipLaunchKernelGGL((kv_attn_kernel<D, true, NT>), grid, dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL((kv_attn_kernel<D, true, NT, W>), grid, dim3(W * kWave), 0, st, a);
   else
-    hipLaunchKernelGGL((kv_attn_kernel<D, false, NT>), grid, dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL((kv_attn_kernel<D, false, NT, W>), grid, dim3(W * kWave), 0, st, a);
 }
 
 template <int D>
@@ -928,8 +930,9 @@ void launch_prompt(const KvAttnArgs &a, bool e4m3, hipStream_t st) {
 }
 
 template <int D>
-hipError_t launch_dim(const KvAttnArgs &a, bool e4m3, int nt, hipStream_t st) {
+hipError_t launch_dim(const KvAttnArgs &a, bool e4m3, int nt, bool wide, hipStream_t st) {
   if (nt == 0) launch_prompt<D>(a, e4m3, st);
+  else if (nt == 1 && wide) launch_decode<D, 1, 8>(a, e4m3, st);
   else if (nt == 1) launch_decode<D, 1>(a, e4m3, st);
   else if (nt == 2 || D == 256) launch_decode<D, 2>(a, e4m3, st);
   else if constexpr (D != 256) launch_decode<D, 4>(a, e4m3, st);
@@ -970,6 +973,10 @@ KvAttnPlan kv_attn_plan(int batch, int heads, int dim, int64_t capacity, int64_t
   // half full on average, hence the share.
   int64_t splits = std::min<int64_t>((4 * slots + base - 1) / base, (span + p.grain - 1) / p.grain);
   if (base >= (p.nt == 0 ? slots : 2 * slots)) splits = 1;
+  // Short sequences, few of them: 8 waves on one piece instead of splits and a
+  // second launch to join them.
+  p.wide = p.nt == 1 && splits > 1 && span <= kWideSpan;
+  if (p.wide) splits = 1;
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(splits, 256));
   p.share = p.splits > 1 ? (int)std::max<int64_t>(slots - base / 2, slots / 2) : 0;
   p.chunk = p.splits > 1 ? p.grain : 1 << 30;
@@ -995,9 +1002,9 @@ hipError_t launch_kv_attention(KvAttnArgs a, bool e4m3, const KvAttnPlan &plan, 
                    ? a.part_o + (size_t)plan.splits * a.s.rows * a.heads_q * a.c.dim
                    : nullptr;
   switch (a.c.dim) {
-    case 64: return launch_dim<64>(a, e4m3, plan.nt, st);
-    case 128: return launch_dim<128>(a, e4m3, plan.nt, st);
-    default: return launch_dim<256>(a, e4m3, plan.nt, st);
+    case 64: return launch_dim<64>(a, e4m3, plan.nt, plan.wide, st);
+    case 128: return launch_dim<128>(a, e4m3, plan.nt, plan.wide, st);
+    default: return launch_dim<256>(a, e4m3, plan.nt, plan.wide, st);
   }
 }
 

@@ -104,6 +104,30 @@ __device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
   }
 }
 
+// x / s, correctly rounded, for many x at one s: with y = fl(1 / s), q = fl(x y)
+// is within an ulp of the quotient, its remainder x - q s is exact in one fused
+// operation, and fl(q + remainder y) is the rounded quotient (Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990).  That
+// needs the remainder above the subnormal range, so it serves 2^-60 <= s <= 2^60
+// (where a quotient too small for that has code 0 either way); other scales
+// divide.  8 divisions a vector took as long as the memory traffic.
+struct Divider {
+  float s, y;
+  bool fast;
+  __device__ __forceinline__ explicit Divider(float scale) : s(scale) {
+    fast = s >= 0x1p-60f && s <= 0x1p60f;
+    y = fast ? 1.f / s : 0.f;
+  }
+  __device__ __forceinline__ float operator()(float x) const {
+    if (fast) {
+      const float q = x * y;
+      // (the sum of a zero remainder and -0 is +0: the sign is x's)
+      return copysignf(__builtin_fmaf(__builtin_fmaf(-q, s, x), y, q), x);
+    }
+    return s > 0.f ? x / s : 0.f;
+  }
+};
+
 struct WriteArgs {
   KvView c;
   SeqView s;
@@ -131,10 +155,31 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(WriteArgs a) {
     float *scale = a.c.scales[kv] + (int64_t)id * a.c.heads + h;
     const float old = part.lo > 0 ? *scale : 0.f;
     const int nvec = (part.hi - part.lo) << vs;
-    float mx = 0.f;
-    for (int i = threadIdx.x; i < nvec; i += kThreads) {
+    // a thread's first kHold vectors stay in registers between the two passes
+    // (a whole page of 64 tokens and 128 dims); more are read again
+    constexpr int kHold = 4;
+    auto at = [&](int i) {
+      return src + (int64_t)(i >> vs) * a.row[kv] + (i & (vpr - 1)) * (8 * Elem<T>::kBytes);
+    };
+    float hold[kHold][8], mx = 0.f;
+#pragma unroll
+    for (int u = 0; u < kHold; ++u) {
+      const int i = threadIdx.x + u * kThreads;
+      if (i < nvec) Elem<T>::load8(at(i), hold[u]);
+      else
+#pragma unroll
+        for (int e = 0; e < 8; ++e) hold[u][e] = 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kHold; ++u)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        hold[u][e] = finite(hold[u][e]);
+        mx = fmaxf(mx, fabsf(hold[u][e]));
+      }
+    for (int i = threadIdx.x + kHold * kThreads; i < nvec; i += kThreads) {
       float x[8];
-      Elem<T>::load8(src + (int64_t)(i >> vs) * a.row[kv] + (i & (vpr - 1)) * (8 * Elem<T>::kBytes), x);
+      Elem<T>::load8(at(i), x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(finite(x[e])));
     }
@@ -145,16 +190,28 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(WriteArgs a) {
 #pragma unroll
     for (int w = 0; w < kThreads / kWave; ++w) mx = fmaxf(mx, red[w]);
     const float s = fmaxf(mx * kStep, old);
-    for (int i = threadIdx.x; i < nvec; i += kThreads) {
-      float x[8];
-      const int r = i >> vs, v = i & (vpr - 1);
-      Elem<T>::load8(src + (int64_t)r * a.row[kv] + v * (8 * Elem<T>::kBytes), x);
+    const Divider by(s);
+    auto put = [&](int i, const float (&x)[8]) {
+      float y[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = s > 0.f ? finite(x[e]) / s : 0.f;
+      for (int e = 0; e < 8; ++e) y[e] = by(x[e]);
       u32x2_t w;
-      w[0] = encode4<E4M3>(x[0], x[1], x[2], x[3]);
-      w[1] = encode4<E4M3>(x[4], x[5], x[6], x[7]);
-      *reinterpret_cast<u32x2_t *>(dst + (int64_t)(part.lo + r) * a.c.token_stride + 8 * v) = w;
+      w[0] = encode4<E4M3>(y[0], y[1], y[2], y[3]);
+      w[1] = encode4<E4M3>(y[4], y[5], y[6], y[7]);
+      *reinterpret_cast<u32x2_t *>(dst + (int64_t)(part.lo + (i >> vs)) * a.c.token_stride +
+                                   8 * (i & (vpr - 1))) = w;
+    };
+#pragma unroll
+    for (int u = 0; u < kHold; ++u) {
+      const int i = threadIdx.x + u * kThreads;
+      if (i < nvec) put(i, hold[u]);
+    }
+    for (int i = threadIdx.x + kHold * kThreads; i < nvec; i += kThreads) {
+      float x[8];
+      Elem<T>::load8(at(i), x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = finite(x[e]);
+      put(i, x);
     }
     if (part.lo > 0 && s > old) {   // older codes of the page move to the new scale
       for (int i = threadIdx.x; i < part.lo << vs; i += kThreads) {

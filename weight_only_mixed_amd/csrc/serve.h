@@ -22,6 +22,7 @@ hipError_t launch_kv_read(const KvView &c, const SeqView &s, bool e4m3, void *k,
 struct KvAttnPlan {
   int nt;         // 16-query tiles per workgroup of the decode kernel; 0: prompt kernel
   int tiles;      // workgroups along a sequence's query rows
+  bool wide;      // 8 waves per workgroup of the decode kernel
   int splits;     // workgroups along the tokens, at most
   int chunk;      // tokens per split, at least
   int grain;      // tokens that splits are multiples of

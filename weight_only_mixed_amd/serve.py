@@ -87,18 +87,18 @@ class KvCache:
 
     def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scales: torch.Tensor,
                  v_scales: torch.Tensor, fmt: int):
-        shape, strides = k_codes.shape, k_codes.stride()
-        _need(k_codes.dtype == v_codes.dtype == torch.uint8 and len(shape) == 4,
-              "KvCache: codes are uint8 [pages, heads, page_size, head_dim]")
-        _need(v_codes.shape == shape and v_codes.stride() == strides and strides[3] == 1,
-              "KvCache: k and v codes need equal shapes and strides, the last dimension contiguous")
+        shape, strides, dev = k_codes.shape, k_codes.stride(), k_codes.device
+        if not (k_codes.dtype == v_codes.dtype == torch.uint8 and len(shape) == 4):
+            _need(False, "KvCache: codes are uint8 [pages, heads, page_size, head_dim]")
+        if not (v_codes.shape == shape and v_codes.stride() == strides and strides[3] == 1):
+            _need(False, "KvCache: k and v codes need equal shapes and strides, the last dimension contiguous")
         pages, heads, page_size, dim = shape
         for s in (k_scales, v_scales):
-            _need(s.dtype == torch.float32 and tuple(s.shape) == (pages, heads) and s.is_contiguous(),
-                  "KvCache: scales are contiguous float32 [pages, heads]")
-        dev = k_codes.device
-        _need(dev.type == "cuda" and v_codes.device == dev and k_scales.device == dev and
-              v_scales.device == dev, "KvCache: all tensors on one GPU")
+            if not (s.dtype == torch.float32 and s.shape == (pages, heads) and s.is_contiguous() and
+                    s.device == dev):
+                _need(False, "KvCache: scales are contiguous float32 [pages, heads] on the codes' GPU")
+        if not (k_codes.is_cuda and v_codes.device == dev):
+            _need(False, "KvCache: all tensors on one GPU")
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.fmt, self.device = fmt, dev
         self.pages, self.heads, self.page_size, self.head_dim = pages, heads, page_size, dim
@@ -123,19 +123,20 @@ class KvSeqs:
     offsets of this step's tokens, the last ones of each sequence)."""
 
     def __init__(self, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor):
-        _need(table.dtype == lens.dtype == cu.dtype == torch.int32, "KvSeqs: int32 tensors")
-        _need(table.dim() == 2 and lens.dim() == 1 and cu.dim() == 1 and
-              cu.shape[0] == lens.shape[0] + 1 and table.shape[0] == lens.shape[0],
-              "KvSeqs: table [batch, max_pages], lens [batch], cu [batch + 1]")
-        batch, width = table.shape
-        stride = table.stride(0) if batch > 1 else width
-        _need((width <= 1 or table.stride(1) == 1) and (batch <= 1 or lens.stride(0) == 1) and
-              (batch < 1 or cu.stride(0) == 1), "KvSeqs: table rows, lens and cu contiguous")
-        dev = table.device
-        _need(dev.type == "cuda" and lens.device == dev and cu.device == dev, "KvSeqs: one GPU")
+        if not (table.dtype == lens.dtype == cu.dtype == torch.int32):
+            _need(False, "KvSeqs: int32 tensors")
+        shape, batch = table.shape, lens.shape[0] if lens.dim() == 1 else -1
+        if not (len(shape) == 2 and shape[0] == batch and cu.shape == (batch + 1,)):
+            _need(False, "KvSeqs: table [batch, max_pages], lens [batch], cu [batch + 1]")
+        width, strides, dev = shape[1], table.stride(), table.device
+        if not ((width <= 1 or strides[1] == 1) and lens.is_contiguous() and cu.is_contiguous()):
+            _need(False, "KvSeqs: table rows, lens and cu contiguous")
+        if not (table.is_cuda and lens.device == dev and cu.device == dev):
+            _need(False, "KvSeqs: one GPU")
         self.table, self.lens, self.cu, self.device = table, lens, cu, dev
         self.batch, self.max_pages = batch, width
-        self._c = _Seqs(batch, width, stride, table.data_ptr(), lens.data_ptr(), cu.data_ptr())
+        self._c = _Seqs(batch, width, strides[0] if batch > 1 else width, table.data_ptr(),
+                        lens.data_ptr(), cu.data_ptr())
         self._ref = ctypes.addressof(self._c)
 
 
