@@ -535,6 +535,7 @@ __global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs
   typedef PromptTile<D> Tile;
   constexpr int TOK = Tile::kTok, GR = Tile::kGroups;
   constexpr int TT = TOK / 32;      // 32-token tiles of S
+  constexpr int ST = TT < 2 ? TT : 2, SG = 2 * ST;   // of these at a time, and their groups
   constexpr int KS = D / 16;        // k steps of q . k
   constexpr int DT = D / 32;        // 32-dim tiles of the output
   __shared__ __attribute__((aligned(16))) unsigned char k_lds[2][Tile::kBytes];
@@ -566,6 +567,11 @@ __global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs
   uint32_t vdst[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) vdst[c] = in_vgpr(Tile::v_at(vd + c, chunk) + part);
+
+  // where a lane reads operands: chunk 2 k + half of K row 32 t + col is at ksrc ^
+  // 32 k, plus t rows of 32, and chunk 2 g + half of V^T row 32 j + col likewise
+  // (a swizzle depends on the row's low bits only)
+  const uint32_t ksrc = Tile::k_at(col, half), vsrc = Tile::v_at(col, half);
 
   // late tiles see the most tokens: they start first
   const int ntiles = (total + kPromptRows - 1) / kPromptRows;
@@ -696,14 +702,19 @@ __global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs
         load(base + TOK, e_next);
         e_next = entry(base + 2 * TOK);
       }
-      if (wave_on && base < any_hi && base + TOK > any_lo) {
-        float f[GR], sv[GR];
-        bool plain = base >= all_lo && base + TOK <= all_hi;
+      // at most 64 tokens at a time: scores and probabilities of more do not fit
+      // beside the accumulators
+#pragma unroll 1
+      for (int sub = 0; sub < TT / ST; ++sub) {
+        const int sbase = base + 32 * ST * sub;
+        if (!wave_on || sbase >= any_hi || sbase + 32 * ST <= any_lo) continue;
+        float f[SG], sv[SG];
+        bool plain = sbase >= all_lo && sbase + 32 * ST <= all_hi;
         float grown = unit;
 #pragma unroll
-        for (int g = 0; g < GR; ++g) {
-          f[g] = sk_lds[buf][g];
-          sv[g] = sv_lds[buf][g];
+        for (int g = 0; g < SG; ++g) {
+          f[g] = sk_lds[buf][SG * sub + g];
+          sv[g] = sv_lds[buf][SG * sub + g];
           plain = plain && f[g] >= 0.f;
           grown = fmaxf(grown, sv[g]);
         }
@@ -716,48 +727,48 @@ __global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs
         }
         // operand reads run kAhead products ahead: the compiler left alone reads
         // each operand right before its product and waits the whole read out
-        constexpr int kAhead = 4, NS = KS * TT, NP = GR * DT;
+        constexpr int kAhead = 4, NS = KS * ST, NP = SG * DT;
         u32x4_t op[kAhead];
         auto k_op = [&](int i) {
           return *reinterpret_cast<const u32x4_t *>(
-              &k_lds[buf][Tile::k_at(32 * (i % TT) + col, 2 * (i / TT) + half)]);
+              &k_lds[buf][(ksrc ^ (uint32_t)(i / ST) << 5) + 32 * (ST * sub + i % ST) * (D * 2)]);
         };
         auto v_op = [&](int i) {
           return *reinterpret_cast<const u32x4_t *>(
-              &v_lds[buf][Tile::v_at(32 * (i % DT) + col, 2 * (i / DT) + half)]);
+              &v_lds[buf][(vsrc ^ (uint32_t)(SG * sub + i / DT) << 5) + 32 * (i % DT) * (TOK * 2)]);
         };
-        f32x16v s[TT];
+        f32x16v s[ST];
 #pragma unroll
-        for (int t = 0; t < TT; ++t) s[t] = f32x16v{};
+        for (int t = 0; t < ST; ++t) s[t] = f32x16v{};
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) op[i] = k_op(i);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-          s[i % TT] = mfma32h(op[i % kAhead], qf[i / TT], s[i % TT]);
+          s[i % ST] = mfma32h(op[i % kAhead], qf[i / ST], s[i % ST]);
           op[i % kAhead] = i + kAhead < NS ? k_op(i + kAhead) : v_op(i + kAhead - NS);
           __builtin_amdgcn_sched_barrier(0);
         }
         // register v of tile t: token 32 t + 8 (v / 4) + 4 half + v % 4, group 2 t + v / 8
         if (__all(plain)) {
 #pragma unroll
-          for (int g = 0; g < GR; ++g) f[g] *= qs;
+          for (int g = 0; g < SG; ++g) f[g] *= qs;
         } else {
 #pragma unroll
-          for (int t = 0; t < TT; ++t)
+          for (int t = 0; t < ST; ++t)
 #pragma unroll
             for (int v = 0; v < 16; ++v) {
-              const int tok = base + 32 * t + 8 * (v >> 2) + 4 * half + (v & 3);
+              const int tok = sbase + 32 * t + 8 * (v >> 2) + 4 * half + (v & 3);
               const bool in = f[2 * t + (v >> 3)] >= 0.f && tok <= pos && tok < tr.hi &&
                               tok >= tr.lo && (a.window <= 0 || tok > pos - a.window);
               s[t][v] = in ? s[t][v] * (f[2 * t + (v >> 3)] * qs) : -INFINITY;
             }
 #pragma unroll
-          for (int g = 0; g < GR; ++g) f[g] = 1.f;
+          for (int g = 0; g < SG; ++g) f[g] = 1.f;
         }
         float mx = -INFINITY;
 #pragma unroll
-        for (int g = 0; g < GR; ++g) {
+        for (int g = 0; g < SG; ++g) {
           float x = s[g >> 1][8 * (g & 1)];
 #pragma unroll
           for (int v = 1; v < 8; ++v) x = fmaxf(x, s[g >> 1][8 * (g & 1) + v]);
@@ -771,9 +782,9 @@ __global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs
           for (int j = 0; j < DT; ++j) acc[j] *= c;
           m = mn;
         }
-        u32x4_t pf[GR];   // one k step of p . v per group of 16 tokens
+        u32x4_t pf[SG];   // one k step of p . v per group of 16 tokens
 #pragma unroll
-        for (int g = 0; g < GR; ++g) {
+        for (int g = 0; g < SG; ++g) {
           const float c = sv[g] * inv_unit;
           float p[8];
 #pragma unroll
