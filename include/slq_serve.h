@@ -137,7 +137,9 @@ size_t slq_kv_attention_workspace_bytes(const slq_kv_cache *cache, const slq_kv_
  * max_q, max_len: the largest n_b and lens[b] the caller expects; they choose
  * the kernel and its grid, results are right for any values >= 1.
  * workspace: as sized above, 256-byte aligned, overwritten; NULL when 0.
- * Sums are taken in a fixed order: repeated calls are bit-identical.
+ * Sums are taken in a fixed order: repeated calls are bit-identical.  Where the
+ * splits fall depends on the hints and on all lengths of the batch, so the last
+ * bits of a sequence's outputs may change with its company.
  */
 slq_status slq_kv_attention(const slq_kv_cache *cache, const slq_kv_seqs *seqs, const void *q,
                             slq_dtype dtype, int64_t rows, int32_t heads_q, int64_t q_row_stride,

@@ -21,6 +21,13 @@
 // tokens of its slots; the byte transposition is part of the conversion.
 // Nothing passes through shared memory before the epilogue.
 //
+// Bound of single tokens: HBM.  Measured, 64 sequences of 300 .. 8192 tokens, 8 kv
+// heads of 4 query heads x 128, INT8 (597 MB): 140 us and 9 us of joining, 4.3 TB/s
+// against 6.3 of a plain read; two sequences of about 131072, 8 query heads per kv
+// head, E4M3 (513 MB): 105 + 9 us, 4.9 TB/s.  Conversions and softmax take about
+// half of the vector issue slots while the loads are out; waves in flight (four per
+// SIMD), not their arithmetic, set the rate.  One sequence of 1003 tokens: 13 us.
+//
 // Probabilities are taken relative to a reference m that a score has reached,
 // and that follows the running maximum only when that has risen by more than
 // 2^4 (otherwise some query of a tile has a new maximum nearly every time, and
@@ -504,6 +511,15 @@ __global__ __launch_bounds__(W *kWave, (D <= 128 && NT == 1 && W == 4 ? 4 : 1)) 
 // other wave.  Rows in shared memory are swizzled in 16-byte chunks so that
 // both the operand reads (neighbouring rows) and the transposed writes (every
 // fourth row) spread over the banks.
+//
+// Measured, 4 x 2048 rows of 4 query heads per kv head against 4212 .. 8192 tokens,
+// 8 kv heads x 128, INT8 (768 GFLOP): 1.00 to 1.14 ms, 670 to 770 TFLOP/s (a large
+// library product reaches 1296 here).  The matrix units are busy for 40% of the
+// cycles and the vector units for 56%; shared memory serves operands in 41%.  With
+// the conversions taken out it takes 0.91 ms instead of 1.18, without softmax 1.04,
+// without both 0.77: operand reads from shared memory, conversion and softmax share
+// the rest.  Two waves of a SIMD half a tile apart behind two barriers a tile (one
+// in its products while the other does softmax) was slower, 1.38 ms against 1.23.
 constexpr int kPromptThreads = 512;
 constexpr int kPromptRows = 256;
 
@@ -844,7 +860,9 @@ __global__ __launch_bounds__(kPromptThreads, 2) void kv_prompt_kernel(KvAttnArgs
   }
 }
 
-// Joins the splits of each query row: one workgroup per row, the splits dealt to
+// Joins the splits of each query row: one workgroup per row (9 us for 2048 rows; with
+// one workgroup per 16 rows and splits read one after another it took 68 us at 128
+// splits), the splits dealt to
 // its four waves (fixed sums: split order within a wave, then wave order).  A
 // row whose tile had no token (no split was active) gets 0 and -inf.
 template <int D>

@@ -7,8 +7,14 @@
 // shared and the result does not depend on any order.
 // The scale is max|x| times the fp32 reciprocal of the largest code (a constant:
 // one multiplication, at most one unit in the last place from the quotient); it
-// is applied with IEEE fp32 divisions, as the weight quantizer's is: a code is
-// the nearest grid point of fl(x / s).
+// is applied as the weight quantizer's is: a code is the nearest grid point of
+// the IEEE fp32 quotient x / s.
+//
+// Bound: HBM for prompts, one chain of dependent reads (offsets, page number,
+// rows) for single tokens.  Measured: 18971 rows of 8 heads x 128 in fp32 to E4M3
+// (194 MB read and written) 43 us, 4.5 TB/s against 5.2 of a plain copy; one token
+// each for 64 sequences 5.6 us.  Reading 112978 rows back as bf16 (694 MB) 139 us,
+// 5.0 TB/s.
 #include <float.h>
 
 #include <algorithm>

@@ -12,15 +12,24 @@
 //     1024 * U consecutive elements and leaves a list of all its elements above
 //     a bound that rises as the unit goes by (about the unit's 16 or 32 largest),
 //     its best element, and where the row's settings need it the unit's mass.
-//  2. sample_pick_kernel, one workgroup per row, sorts the listed elements above
-//     the largest of the row's bounds (everything above it is listed): a sorted
-//     prefix of the row, usually hundreds of elements long.  A kept set that
-//     ends inside it is cut there and drawn from.  Without any cut the units'
-//     masses name the unit, and only that is read again.  A kept set that ends
-//     outside (a wide nucleus, thousands of ties) is found by a radix descent
-//     over the 32-bit ordered keys of the row with a (count, mass) histogram
-//     per digit, and drawn by a descent over index segments.
+//  2. sample_pick_kernel, one workgroup per row, takes the listed elements above
+//     the largest of the row's bounds: all of the row's elements above it, so a
+//     prefix of the order, usually hundreds of elements long.  A kept set that
+//     ends inside it is narrowed down by a histogram of keys, cut and drawn from
+//     there, by comparing all pairs (up to kPairs elements: 16 us for a row
+//     where sorting the whole prefix took 31) or by sorting.  Without any cut the
+//     units' masses name the unit, and only that is read again.  A kept set that
+//     ends outside (a wide nucleus) is found from a histogram of the row's values
+//     and the one bin where the cut falls, or (a bin of thousands of ties) by a
+//     radix descent over the 32-bit ordered keys, and drawn by a descent over
+//     index segments.
 // A row of at most kList elements needs no first launch: it is sorted whole.
+//
+// Bound: HBM for many rows, latency for few.  Measured (kernel times): 512 rows of
+// 151936 in fp32 (311 MB) 67 us for the lists, 4.6 TB/s, and 33 for the picks; one
+// such row 6 + 16 us.  A wide nucleus costs the row's workgroup two passes of 64-bit
+// exponentials over the row: 64 rows of 50257 in bf16 of which a fifth have one take
+// 11 + 89 us.
 #include <float.h>
 
 #include <algorithm>
