@@ -372,6 +372,70 @@ def test_attention_not_a_number(new):
         assert bool(torch.isnan(lse[0, 1])) and int(torch.isnan(lse).sum()) == 1
 
 
+MORE = [
+    # page, dim, heads, group, lens, new, window: many short sequences; many kv heads; a
+    # group wider than any tile; long contexts under few prompt rows; lens behind the table
+    (16, 64, 2, 3, list(range(0, 310)), [1] * 310, 0),
+    (16, 64, 300, 1, [40, 7], [1, 7], 0),
+    (32, 64, 1, 300, [65, 33], [2, 1], 16),
+    (64, 128, 1, 4, [3000, 2900], [40, 33], 0),
+    (64, 128, 1, 4, [3000, 2900], [40, 33], 2500),
+    (16, 256, 1, 5, [1500], [50], 700),
+    (16, 64, 1, 20, [2000, 1], [1, 1], 5000),
+]
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("case", range(len(MORE)))
+def test_attention_unusual_batches(fmt, case):
+    page, dim, heads, group, lens, new, window = MORE[case]
+    g = np.random.default_rng(100 + case)
+    lens, new = np.array(lens), np.minimum(np.array(new), lens)
+    table, pages = tables(g, lens, page)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    box = Box(pages, heads, dim, page, fmt, seed=case, fill="values")
+    q = rand(g, (int(cu[-1]), heads * group, dim), "bf16", 1.5)
+    sc = float(np.float32(1 / np.sqrt(dim)))
+    ref = orc.kv_attention(box.codes[0], box.scales[0], box.codes[1], box.scales[1], table, lens, cu,
+                           q.float().cpu().numpy(), box.fmt, sc, window)
+    for kw in (dict(max_q=int(new.max()), max_len=int(lens.max())), {}, dict(max_q=1, max_len=1), dict(max_len=10 ** 12)):
+        check_attention(box, table, lens, cu, q, window, what=f"unusual {case} {kw}", oracle=ref, **kw)
+
+
+@pytest.mark.parametrize("new", [1, 90])
+def test_attention_lengths_behind_the_table(new):
+    """A length that the table has no pages for: what the table holds is seen, by
+    queries whose positions lie behind it too."""
+    g = np.random.default_rng(new)
+    box = Box(6, 1, 64, 16, "int8", fill="values")
+    table = np.array([[0, 1, 2], [3, 4, 5]])
+    q = rand(g, (2 * new, 2, 64), "bf16")
+    for lens in ([60, 48], [1000, 2 ** 31 - 1], [-5, 47]):
+        check_attention(box, table, np.array(lens), np.array([0, new, 2 * new]), q, max_q=new, what=f"lens {lens}")
+        check_attention(box, table, np.array(lens), np.array([0, new, 2 * new]), q, window=30, what=f"lens {lens} window")
+
+
+def test_two_streams_at_once():
+    """Calls of different shapes in flight on two streams, each with its own workspace."""
+    g = np.random.default_rng(33)
+    jobs = []
+    for n, new in ((3000, 1), (1500, 80)):
+        box = Box(200, 2, 128, 16, "int8", seed=n, fill="values")
+        s = gseqs(g.permutation(188)[None], [n], [0, new])
+        q = rand(g, (new, 8, 128), "bf16")
+        jobs.append((box, s, q, slq.slq_kv_attention(box.dev, s, q, max_q=new, max_len=n, with_lse=True), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = []
+        for box, s, q, _, stream in jobs:
+            with torch.cuda.stream(stream):
+                got.append(slq.slq_kv_attention(box.dev, s, q, max_q=q.shape[0], max_len=3008, with_lse=True))
+        torch.cuda.synchronize()
+        for (box, s, q, ref, _), (o, lse) in zip(jobs, got):
+            assert float((o.float() - ref[0].float()).abs().max()) <= 2.0 ** -6 * float(ref[0].float().abs().max())
+            assert float((lse - ref[1]).abs().max()) <= 1e-4
+
+
 def test_attention_strided_queries():
     g = np.random.default_rng(6)
     box = Box(4, 2, 64, 32, "e4m3", seed=2, fill="values")

@@ -178,6 +178,39 @@ def test_more_rows_than_compute_units():
     check(logits, u, "rows", **settings(g, 5000, 300)["all"])
 
 
+@pytest.mark.parametrize("vocab", [2041, 2047, 2048, 2049, 2050, 4095, 8193])
+@pytest.mark.parametrize("dtype", ["fp32", "fp16"])
+def test_sizes_around_the_whole_row_list(vocab, dtype):
+    g = np.random.default_rng(vocab)
+    logits = rows_of(g, 3, vocab, dtype)
+    u = g.random(3).astype(np.float32)
+    for what, cuts in settings(g, 3, vocab).items():
+        check(logits, u, what, **cuts)
+
+
+def test_very_many_rows():
+    g = np.random.default_rng(41)
+    logits = torch.from_numpy((g.standard_normal((70000, 12)) * 2).astype(np.float32)).to(DEV)
+    check(logits, g.random(70000).astype(np.float32), "rows", **settings(g, 70000, 12)["top-p"])
+
+
+def test_two_streams_at_once():
+    g = np.random.default_rng(43)
+    a, b = rows_of(g, 6, 40009, "fp32"), rows_of(g, 50, 9001, "bf16")
+    ua, ub = (torch.from_numpy(g.random(n).astype(np.float32)).to(DEV) for n in (6, 50))
+    pa, pb = torch.full((6,), 0.95, device=DEV), torch.full((50,), 0.6, device=DEV)
+    ra, rb = slq.slq_sample(a, ua, top_p=pa), slq.slq_sample(b, ub, top_p=pb)
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        with torch.cuda.stream(s[0]):
+            ta = slq.slq_sample(a, ua, top_p=pa)
+        with torch.cuda.stream(s[1]):
+            tb = slq.slq_sample(b, ub, top_p=pb)
+        torch.cuda.synchronize()
+        assert torch.equal(ta[0], ra[0]) and torch.equal(tb[0], rb[0]) and torch.equal(tb[1], rb[1])
+
+
 def test_graph_replays_with_eager_calls_between():
     g = np.random.default_rng(31)
     logits, u = rows_of(g, 4, 30011, "fp32"), torch.zeros(4, device=DEV)

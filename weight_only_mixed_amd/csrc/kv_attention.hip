@@ -174,8 +174,8 @@ __device__ __forceinline__ TileRange tile_range(const KvAttnArgs &a, const KvSpa
   TileRange t;
   t.lo = r.lo;
   t.hi = r.hi;
-  t.start = r.lo & ~(kBlock - 1);
-  const int n = r.hi > r.lo ? r.hi - t.start : 0;
+  t.start = r.hi > r.lo ? r.lo & ~(kBlock - 1) : r.hi;   // nothing to walk where empty
+  const int n = r.hi - t.start;
   // as many splits as `size` asks for, within the grid, of equal size
   const int want = min(max((n - 1) / size + 1, 1), a.splits);
   t.chunk = ((n - 1) / want + a.grain) / a.grain * a.grain;

@@ -94,10 +94,12 @@ struct KvRange {
 SLQ_HD KvRange kv_visible(const KvSpan &s, int32_t window, int32_t i0, int32_t i1) {
   const int32_t end = s.pos0 + i1 + 1;
   KvRange r;
-  r.hi = end < s.len ? end : s.len;
+  r.hi = end < s.len ? (end > 0 ? end : 0) : s.len;
   const int32_t first = s.pos0 + i0;
   r.lo = window > 0 && first >= window ? first - window + 1 : 0;
-  if (r.hi < r.lo) r.hi = r.lo;
+  // an empty range lies within the tokens too: positions behind them reach 2^31,
+  // where a walk in steps of a block would pass the range of int
+  if (r.lo > r.hi) r.lo = r.hi;
   return r;
 }
 

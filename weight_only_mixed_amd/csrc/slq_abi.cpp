@@ -498,7 +498,7 @@ const char *slq_strerror(slq_status s) {
   switch (s) {
     case SLQ_OK: return "ok";
     case SLQ_EINVAL: return "invalid argument (size, bit-width, pointer, alignment or aliasing)";
-    case SLQ_ENOTSUP: return "unsupported request (group size other than 128)";
+    case SLQ_ENOTSUP: return "unsupported request (group size other than 128; serving: head size, page size or type)";
     case SLQ_EHIP: return "HIP runtime error at launch";
     case SLQ_ESCRATCH:
       return "the request needs more split-k scratch than the allocation-free entry point holds";
