@@ -402,6 +402,22 @@ def test_attention_unusual_batches(fmt, case):
         check_attention(box, table, lens, cu, q, window, what=f"unusual {case} {kw}", oracle=ref, **kw)
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_attention_more_tiles_than_the_grid(fmt, dim):
+    """Every width of the decode kernel's query tile, and sequences with more rows
+    than its grid covers in one pass (a batch whose other sequences are empty)."""
+    g = np.random.default_rng(dim)
+    box = Box(30, 1, dim, 16, fmt, seed=1, fill="values")
+    for new, hint in ((17, 17), (33, 33), (45, 45), (64, 64), (100, 45), (130, 64), (100, 20), (70, 30), (100, 10)):
+        batch = -(-new // hint)
+        table = np.concatenate([g.permutation(30)[None]] * batch)
+        lens, cu = np.array([170] + [0] * (batch - 1)), np.array([0] + [new] * batch)
+        q = rand(g, (new, 1, dim), "bf16", 1.5)
+        for max_len in (1, 480):
+            check_attention(box, table, lens, cu, q, max_q=hint, max_len=max_len, what=f"{dim} {new} rows, {hint} expected")
+
+
 @pytest.mark.parametrize("new", [1, 90])
 def test_attention_lengths_behind_the_table(new):
     """A length that the table has no pages for: what the table holds is seen, by

@@ -963,8 +963,11 @@ hipError_t launch_dim(const KvAttnArgs &a, bool e4m3, int nt, bool wide, hipStre
   if (nt == 0) launch_prompt<D>(a, e4m3, st);
   else if (nt == 1 && wide) launch_decode<D, 1, 8>(a, e4m3, st);
   else if (nt == 1) launch_decode<D, 1>(a, e4m3, st);
-  else if (nt == 2 || D == 256) launch_decode<D, 2>(a, e4m3, st);
-  else if constexpr (D != 256) launch_decode<D, 4>(a, e4m3, st);
+  else if (nt == 2) {
+    if constexpr (D <= 128) launch_decode<D, 2>(a, e4m3, st);
+  } else if constexpr (D == 64) {
+    launch_decode<D, 4>(a, e4m3, st);
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   const int tile_rows = nt == 0 ? kPromptRows : 16 * nt;
@@ -984,7 +987,12 @@ KvAttnPlan kv_attn_plan(int batch, int heads, int dim, int64_t capacity, int64_t
   const int64_t q = std::min(max_q, rows);
   const int64_t qrows = q * group;
   p.rows = (int)std::min<int64_t>(qrows, 65535);
-  p.nt = qrows <= 16 ? 1 : qrows <= 32 || (dim == 256 && qrows <= 64) ? 2 : qrows <= 64 ? 4 : 0;
+  // As many query tiles per workgroup as the accumulators of 256 vector registers
+  // allow.  (Wider instances, four tiles of 128 dims or two of 256, overflowed into
+  // the accumulation registers; built with results in vector registers, those gave
+  // wrong rows in the second pass of their tile loop.)
+  const int widest = dim == 64 ? 4 : dim == 128 ? 2 : 1;
+  p.nt = qrows > 64 ? 0 : std::min(widest, qrows <= 16 ? 1 : qrows <= 32 ? 2 : 4);
   const int tile_rows = p.nt == 0 ? kPromptRows : 16 * p.nt;
   p.tiles = (int)std::min<int64_t>((qrows + tile_rows - 1) / tile_rows, 65535);
   int64_t span = std::min(max_len, capacity);
