@@ -120,6 +120,17 @@ def test_attention_refusals():
     assert attn(s=seqs(batch=0)) == OK and attn(rows=0, ws=None) == OK
 
 
+def test_attention_workspace_sizes():
+    """A few rows split over long tokens need one; a hint that contradicts the rows
+    does not make it large; short and wide calls need none."""
+    def size(rows, mq, ml, batch=1, hq=32):
+        c, s = cache(), seqs(batch=batch, width=1 << 14)
+        return slq.lib().slq_kv_attention_workspace_bytes(ctypes.addressof(c), ctypes.addressof(s), rows, hq, 0, mq, ml)
+    assert 0 < size(1, 1, 1 << 20) <= 256 * 32 * 129 * 4
+    assert size(1, 1, 100) == 0 and size(64, 1, 4000, batch=64) > 0 and size(1000, 1, 10 ** 6, batch=1000) == 0
+    assert size(1 << 20, 1, 1 << 20) == 0 and size(1 << 20, 1 << 20, 1 << 20) == 0
+
+
 def test_sample_refusals():
     for kw in (dict(dtype=3), dict(rows=-1), dict(rows=1 << 22), dict(vocab=0), dict(vocab=(1 << 24) + 1), dict(stride=-1),
                dict(logits=None), dict(u=None), dict(tok=None), dict(logits=P[0] + 2), dict(u=P[1] + 1), dict(t=P[2] + 2),

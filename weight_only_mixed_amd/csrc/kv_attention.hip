@@ -984,7 +984,9 @@ KvAttnPlan kv_attn_plan(int batch, int heads, int dim, int64_t capacity, int64_t
                         int window, int64_t max_q, int64_t max_len) {
   KvAttnPlan p{};
   const int64_t group = heads_q / heads;
-  const int64_t q = std::min(max_q, rows);
+  // some sequence has at least its share of the rows, whatever max_q says (and
+  // the workspace of splits is for all rows)
+  const int64_t q = std::max(std::min(max_q, rows), (rows + batch - 1) / batch);
   const int64_t qrows = q * group;
   p.rows = (int)std::min<int64_t>(qrows, 65535);
   // As many query tiles per workgroup as the accumulators of 256 vector registers
